@@ -567,6 +567,87 @@ int h3b_gemm_bf16_ln(const h3b_bf16* A, const h3b_bf16* B, int M, int N, int K, 
 int h3b_attention(const h3b_bf16* qkv, int n_tokens, int n_heads, int head_dim,
                   h3b_bf16* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- operators on heads
+ * Operators on q and k (and on attention over them) outside the block's fixed layout: any
+ * strided view, explicit positions, shared key heads, 16- and 32-bit types.  No counterpart
+ * on the pages: what a caller needs next to the block to run batches of clips of different
+ * sizes, clips that continue another one, or a training step of the Q/K norms. */
+
+/* Element types of the operators that take one. */
+enum { H3B_DT_BF16 = 0, H3B_DT_F16 = 1, H3B_DT_F32 = 2 };
+
+/* A [batch, tokens, heads, head_dim] device tensor: its first element and its strides in
+ * elements; head_dim is contiguous.  data must be 16-byte aligned and every stride a
+ * non-negative multiple of 16 bytes (the stride of a dimension of size 1 is ignored, and so
+ * is batch_stride where there is no batch).  An input may have stride 0 where it is
+ * broadcast; an output's elements must not overlap. */
+typedef struct h3b_head_view {
+  const void* data;
+  long long batch_stride, token_stride, head_stride;
+} h3b_head_view;
+
+/* Rotary positions with several axes (time, height, width, ...), written by
+ * h3b_rope_plan_make and then read-only.  Pair p of a head turns by
+ * 2 pi * pos[axis[p]] * turns[p]. */
+enum { H3B_ROPE_ADJACENT = 0, H3B_ROPE_HALVES = 1 };
+enum { H3B_ROPE_MAX_PAIRS = 128, H3B_ROPE_MAX_AXES = 4 };
+typedef struct h3b_rope_plan {
+  unsigned magic;                       /* set by h3b_rope_plan_make */
+  int n_axes, n_pairs, pairing;
+  unsigned char axis[H3B_ROPE_MAX_PAIRS];
+  double turns[H3B_ROPE_MAX_PAIRS];     /* revolutions per unit of position */
+} h3b_rope_plan;
+
+/* Fill a plan (host).  split[a], even and non-negative, is the width of axis a in channels;
+ * the first R = sum(split) <= 256 channels of a head are rotated, the rest pass through.
+ * Pairs are numbered axis by axis.  pairing: H3B_ROPE_ADJACENT (channels 2p, 2p + 1) or
+ * H3B_ROPE_HALVES (channels p, p + R/2; R % 8 == 0).  With k the pair's index inside its
+ * axis, its frequency is theta^(-2k / split[a]), or, shared_freq != 0, theta^(-2p / R): one
+ * ladder over all axes.  h3b_rope_table's rotation is ADJACENT with shared_freq == 0. */
+int h3b_rope_plan_make(int n_axes, const int* split, float theta, int pairing, int shared_freq,
+                       h3b_rope_plan* plan);
+
+/* out = x rotated at the tokens' positions (inverse == 0), or turned back (inverse != 0),
+ * which is also the gradient of the rotation: the gradient of x from that of out.
+ * x, out: [batch, n_tokens, n_heads, head_dim] of type dtype; head_dim % 8 == 0, at least
+ * the plan's rotated width, at most 256.  pos (device, fp32): [n_tokens, n_axes] of each
+ * sequence, pos_batch_stride elements apart (0: the sequences share their positions); finite.
+ * The angle of a position is exact to 64 bits, the rest is in fp32 with one rounding.
+ * out may be x itself (the same view), else they must not overlap. */
+int h3b_rope_axes(const h3b_rope_plan* plan, int dtype, const h3b_head_view* x, int batch,
+                  int n_tokens, int n_heads, int head_dim, const float* pos,
+                  long long pos_batch_stride, int inverse, const h3b_head_view* out,
+                  void* stream);
+
+/* Per-head RMS norm of q and k with the rotation in the same pass:
+ *   y = R(x / sqrt(mean(x^2) + eps) * gain)          per token and head.
+ * q, q_out [batch, n_tokens, n_q_heads, head_dim], k, k_out with n_k_heads (0: no k, its
+ * arguments are ignored); gains [head_dim] fp32 (device; NULL = ones).  plan == NULL: no
+ * rotation (pos is ignored).  Sizes, positions, rounding and in-place use as h3b_rope_axes. */
+int h3b_qk_norm_rope(const h3b_rope_plan* plan, int dtype, const h3b_head_view* q,
+                     const h3b_head_view* k, int batch, int n_tokens, int n_q_heads,
+                     int n_k_heads, int head_dim, const float* q_gain, const float* k_gain,
+                     float eps, const float* pos, long long pos_batch_stride,
+                     const h3b_head_view* q_out, const h3b_head_view* k_out, void* stream);
+
+/* Bytes of workspace h3b_qk_norm_rope_backward needs (0 on a bad head_dim). */
+size_t h3b_qk_norm_rope_backward_workspace_size(int head_dim);
+
+/* The backward pass of h3b_qk_norm_rope: from its inputs q, k and the gradients g_q, g_k of
+ * its outputs, the gradients dq, dk (overwritten) and those of the gains dq_gain, dk_gain
+ * [head_dim] fp32 (overwritten; NULL = not wanted).  dq may be q or g_q itself (the same
+ * view), dk likewise; otherwise outputs must not overlap inputs.  The gains' gradients are
+ * summed in fp32 in a fixed order: equal calls give equal bits.  ws: device, 16-byte aligned,
+ * h3b_qk_norm_rope_backward_workspace_size bytes, used by one call at a time. */
+int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_head_view* q,
+                              const h3b_head_view* k, int batch, int n_tokens, int n_q_heads,
+                              int n_k_heads, int head_dim, const float* q_gain,
+                              const float* k_gain, float eps, const float* pos,
+                              long long pos_batch_stride, const h3b_head_view* g_q,
+                              const h3b_head_view* g_k, const h3b_head_view* dq,
+                              const h3b_head_view* dk, float* dq_gain, float* dk_gain, void* ws,
+                              size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- host policy */
 /* Layer thinning mask (dothoosh.com "Aggressive optimisation levers": rank blocks by
  * their AdaLN gates, always keep the first and last block).  score_b = mean|gate_msa| +

@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -165,6 +166,83 @@ int check_fold(const h3b_block_weights* w) {
   const void* p[6] = {w->w_qkv_fold, w->c_qkv, w->d_qkv, w->w_fc1_fold, w->c_fc1, w->d_fc1};
   for (const void* q : p)
     if (!al16(q)) return set_error(H3B_EINVAL, "folded weight pointer not 16-byte aligned");
+  return H3B_OK;
+}
+
+constexpr unsigned kRopePlanMagic = 0x68335250u;
+
+inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// The caller's view as the kernels take it: strides of dimensions of size 1 become 0.
+int head_view(const char* who, const char* name, const h3b_head_view* v, int dtype, int batch,
+              int tokens, int heads, bool output, HeadView* out) {
+  if (heads == 0 || tokens == 0 || batch == 0) return H3B_OK;
+  if (!v || !v->data || !al16(v->data))
+    return set_error(H3B_EINVAL, "%s: %s is NULL or not 16-byte aligned", who, name);
+  const long long st[3] = {batch > 1 ? v->batch_stride : 0, tokens > 1 ? v->token_stride : 0,
+                           heads > 1 ? v->head_stride : 0};
+  const int size[3] = {batch, tokens, heads};
+  const long long unit = dtype == H3B_DT_F32 ? 4 : 8;
+  for (int i = 0; i < 3; ++i) {
+    if (st[i] < 0 || st[i] % unit || st[i] > (1ll << 38))
+      return set_error(H3B_EINVAL, "%s: %s: stride %lld must be a non-negative multiple of 16 bytes",
+                       who, name, st[i]);
+    if (output && size[i] > 1 && st[i] == 0)
+      return set_error(H3B_EINVAL, "%s: %s is an output and has stride 0", who, name);
+  }
+  *out = HeadView{const_cast<void*>(v->data), st[0], st[1], st[2]};
+  return H3B_OK;
+}
+
+// Sizes, types, plan and positions of the operators on heads.
+int head_rows_common(const char* who, const h3b_rope_plan* plan, int dtype, int batch, int tokens,
+                     int q_heads, int k_heads, int head_dim, const float* pos,
+                     long long pos_batch_stride, HeadRows* a) {
+  if (dtype != H3B_DT_BF16 && dtype != H3B_DT_F16 && dtype != H3B_DT_F32)
+    return set_error(H3B_EINVAL, "%s: unknown dtype %d", who, dtype);
+  if (batch < 0 || tokens < 0 || q_heads < 0 || k_heads < 0 || q_heads > 65536 || k_heads > 65536)
+    return set_error(H3B_EINVAL, "%s: bad sizes (batch=%d tokens=%d heads=%d, %d)", who, batch,
+                     tokens, q_heads, k_heads);
+  if (head_dim < 8 || head_dim > 256 || head_dim % 8)
+    return set_error(H3B_EINVAL, "%s: head_dim %d must be a multiple of 8 in 8..256", who, head_dim);
+  a->tokens = tokens;
+  a->rows = 1ll * batch * tokens;
+  a->heads[0] = q_heads;
+  a->heads[1] = k_heads;
+  a->head_dim = head_dim;
+  if (!plan) return H3B_OK;
+  if (plan->magic != kRopePlanMagic || plan->n_pairs < 1 || plan->n_pairs > H3B_ROPE_MAX_PAIRS ||
+      plan->n_axes < 1 || plan->n_axes > H3B_ROPE_MAX_AXES)
+    return set_error(H3B_EINVAL, "%s: the plan was not made by h3b_rope_plan_make", who);
+  if (2 * plan->n_pairs > head_dim)
+    return set_error(H3B_EINVAL, "%s: the plan rotates %d channels of a head of %d", who,
+                     2 * plan->n_pairs, head_dim);
+  if (a->rows > 0 && (!pos || !al4(pos)))
+    return set_error(H3B_EINVAL, "%s: pos is NULL or misaligned", who);
+  if (pos_batch_stride < 0)
+    return set_error(H3B_EINVAL, "%s: pos_batch_stride is negative", who);
+  a->pos = pos;
+  a->pos_batch = pos_batch_stride;
+  a->n_axes = plan->n_axes;
+  a->n_pairs = plan->n_pairs;
+  for (int i = 0; i < plan->n_pairs; ++i) {
+    if (plan->axis[i] >= plan->n_axes)
+      return set_error(H3B_EINVAL, "%s: the plan was not made by h3b_rope_plan_make", who);
+    a->axis[i] = plan->axis[i];
+    a->turns[i] = plan->turns[i];
+  }
+  return H3B_OK;
+}
+
+int head_rows_gains(const char* who, float eps, const float* q_gain, const float* k_gain,
+                    HeadRows* a) {
+  if (!(eps > 0.f) || !std::isfinite(eps))
+    return set_error(H3B_EINVAL, "%s: eps must be positive and finite", who);
+  if (!al4(q_gain) || !al4(k_gain))
+    return set_error(H3B_EINVAL, "%s: misaligned gains", who);
+  a->q_gain = q_gain;
+  a->k_gain = k_gain;
+  a->eps = eps;
   return H3B_OK;
 }
 
@@ -1471,6 +1549,131 @@ int h3b_attention(const h3b_bf16* qkv, int n_tokens, int n_heads, int head_dim, 
   if (int rc = get_ctx(&ctx)) return rc;
   return launch_attention(ctx, reinterpret_cast<const bf16*>(qkv), n_tokens, n_heads, head_dim,
                           reinterpret_cast<bf16*>(out), ws, ws_bytes,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int h3b_rope_plan_make(int n_axes, const int* split, float theta, int pairing, int shared_freq,
+                       h3b_rope_plan* plan) {
+  if (!plan) return set_error(H3B_EINVAL, "rope_plan_make: plan is NULL");
+  if (n_axes < 1 || n_axes > H3B_ROPE_MAX_AXES || !split)
+    return set_error(H3B_EINVAL, "rope_plan_make: n_axes=%d must be in 1..%d", n_axes,
+                     H3B_ROPE_MAX_AXES);
+  if (pairing != H3B_ROPE_ADJACENT && pairing != H3B_ROPE_HALVES)
+    return set_error(H3B_EINVAL, "rope_plan_make: unknown pairing %d", pairing);
+  if (!(theta > 0.f) || !std::isfinite(theta))
+    return set_error(H3B_EINVAL, "rope_plan_make: theta must be positive and finite");
+  int width = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (split[a] < 0 || (split[a] & 1) || split[a] > 2 * H3B_ROPE_MAX_PAIRS)
+      return set_error(H3B_EINVAL, "rope_plan_make: split[%d]=%d must be even, in 0..%d", a,
+                       split[a], 2 * H3B_ROPE_MAX_PAIRS);
+    width += split[a];
+  }
+  if (width < 2 || width > 2 * H3B_ROPE_MAX_PAIRS)
+    return set_error(H3B_EINVAL, "rope_plan_make: the rotated width %d must be in 2..%d", width,
+                     2 * H3B_ROPE_MAX_PAIRS);
+  if (pairing == H3B_ROPE_HALVES && width % 8)
+    return set_error(H3B_EINVAL, "rope_plan_make: half-split pairs need a width (%d) that is a multiple of 8", width);
+  h3b_rope_plan p = {};
+  p.magic = kRopePlanMagic;
+  p.n_axes = n_axes;
+  p.n_pairs = width / 2;
+  p.pairing = pairing;
+  int i = 0;
+  for (int a = 0; a < n_axes; ++a)
+    for (int k = 0; k < split[a] / 2; ++k, ++i) {
+      const double e = shared_freq ? 2.0 * i / width : 2.0 * k / split[a];
+      p.axis[i] = static_cast<unsigned char>(a);
+      p.turns[i] = std::pow(static_cast<double>(theta), -e) / 6.283185307179586476925;
+    }
+  *plan = p;
+  return H3B_OK;
+}
+
+int h3b_rope_axes(const h3b_rope_plan* plan, int dtype, const h3b_head_view* x, int batch,
+                  int n_tokens, int n_heads, int head_dim, const float* pos,
+                  long long pos_batch_stride, int inverse, const h3b_head_view* out,
+                  void* stream) {
+  HeadRows a;
+  int rc;
+  if (!plan) return set_error(H3B_EINVAL, "rope_axes: plan is NULL");
+  if ((rc = head_rows_common("rope_axes", plan, dtype, batch, n_tokens, n_heads, 0, head_dim, pos,
+                             pos_batch_stride, &a)) ||
+      (rc = head_view("rope_axes", "x", x, dtype, batch, n_tokens, n_heads, false, &a.in[0])) ||
+      (rc = head_view("rope_axes", "out", out, dtype, batch, n_tokens, n_heads, true, &a.out[0])))
+    return rc;
+  a.inverse = inverse != 0;
+  DevCtx ctx;
+  if ((rc = get_ctx(&ctx))) return rc;
+  if (a.rows == 0 || n_heads == 0) return H3B_OK;
+  return launch_head_rows(ctx, dtype, 0, a, plan->pairing == H3B_ROPE_HALVES,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int h3b_qk_norm_rope(const h3b_rope_plan* plan, int dtype, const h3b_head_view* q,
+                     const h3b_head_view* k, int batch, int n_tokens, int n_q_heads,
+                     int n_k_heads, int head_dim, const float* q_gain, const float* k_gain,
+                     float eps, const float* pos, long long pos_batch_stride,
+                     const h3b_head_view* q_out, const h3b_head_view* k_out, void* stream) {
+  const char* me = "qk_norm_rope";
+  HeadRows a;
+  int rc;
+  if ((rc = head_rows_common(me, plan, dtype, batch, n_tokens, n_q_heads, n_k_heads, head_dim, pos,
+                             pos_batch_stride, &a)) ||
+      (rc = head_rows_gains(me, eps, q_gain, k_gain, &a)) ||
+      (rc = head_view(me, "q", q, dtype, batch, n_tokens, n_q_heads, false, &a.in[0])) ||
+      (rc = head_view(me, "k", k, dtype, batch, n_tokens, n_k_heads, false, &a.in[1])) ||
+      (rc = head_view(me, "q_out", q_out, dtype, batch, n_tokens, n_q_heads, true, &a.out[0])) ||
+      (rc = head_view(me, "k_out", k_out, dtype, batch, n_tokens, n_k_heads, true, &a.out[1])))
+    return rc;
+  DevCtx ctx;
+  if ((rc = get_ctx(&ctx))) return rc;
+  if (a.rows == 0 || n_q_heads + n_k_heads == 0) return H3B_OK;
+  return launch_head_rows(ctx, dtype, 1, a, plan && plan->pairing == H3B_ROPE_HALVES,
+                          static_cast<cudaStream_t>(stream));
+}
+
+size_t h3b_qk_norm_rope_backward_workspace_size(int head_dim) {
+  if (head_dim <= 0 || head_dim > 256 || head_dim % 8) {
+    set_error(H3B_EINVAL, "qk_norm_rope_backward: head_dim %d must be a multiple of 8 in 8..256",
+              head_dim);
+    return 0;
+  }
+  return head_rows_bwd_bytes(head_dim);
+}
+
+int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_head_view* q,
+                              const h3b_head_view* k, int batch, int n_tokens, int n_q_heads,
+                              int n_k_heads, int head_dim, const float* q_gain,
+                              const float* k_gain, float eps, const float* pos,
+                              long long pos_batch_stride, const h3b_head_view* g_q,
+                              const h3b_head_view* g_k, const h3b_head_view* dq,
+                              const h3b_head_view* dk, float* dq_gain, float* dk_gain, void* ws,
+                              size_t ws_bytes, void* stream) {
+  const char* me = "qk_norm_rope_backward";
+  HeadRows a;
+  int rc;
+  if ((rc = head_rows_common(me, plan, dtype, batch, n_tokens, n_q_heads, n_k_heads, head_dim, pos,
+                             pos_batch_stride, &a)) ||
+      (rc = head_rows_gains(me, eps, q_gain, k_gain, &a)) ||
+      (rc = head_view(me, "q", q, dtype, batch, n_tokens, n_q_heads, false, &a.in[0])) ||
+      (rc = head_view(me, "k", k, dtype, batch, n_tokens, n_k_heads, false, &a.in[1])) ||
+      (rc = head_view(me, "g_q", g_q, dtype, batch, n_tokens, n_q_heads, false, &a.grad[0])) ||
+      (rc = head_view(me, "g_k", g_k, dtype, batch, n_tokens, n_k_heads, false, &a.grad[1])) ||
+      (rc = head_view(me, "dq", dq, dtype, batch, n_tokens, n_q_heads, true, &a.out[0])) ||
+      (rc = head_view(me, "dk", dk, dtype, batch, n_tokens, n_k_heads, true, &a.out[1])))
+    return rc;
+  if (!al4(dq_gain) || !al4(dk_gain))
+    return set_error(H3B_EINVAL, "%s: misaligned gain gradient", me);
+  if (!ws || !al16(ws) || ws_bytes < head_rows_bwd_bytes(head_dim))
+    return set_error(H3B_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given (16-byte aligned)",
+                     me, head_rows_bwd_bytes(head_dim), ws ? ws_bytes : size_t(0));
+  a.part = static_cast<float*>(ws);
+  a.dq_gain = dq_gain;
+  a.dk_gain = dk_gain;
+  DevCtx ctx;
+  if ((rc = get_ctx(&ctx))) return rc;
+  return launch_head_rows(ctx, dtype, 2, a, plan && plan->pairing == H3B_ROPE_HALVES,
                           static_cast<cudaStream_t>(stream));
 }
 

@@ -151,6 +151,48 @@ int launch_attention(const DevCtx& ctx, const bf16* qkv, int n_tokens, int n_hea
 // 2 two tiles; -1 on a bad value.
 int set_attention_variant(int v);
 
+// ---------------------------------------------------------------- head operators
+// A [batch, tokens, heads, head_dim] tensor by its strides in elements (head_dim contiguous).
+struct HeadView {
+  void* data = nullptr;
+  long long batch = 0, token = 0, head = 0;
+};
+
+// Rotation and per-head RMS norm over the heads of q ([0]) and k ([1]).
+struct HeadRows {
+  HeadView in[2], grad[2], out[2];  // grad: the output's gradient (backward only)
+  int heads[2] = {0, 0};
+  int head_dim = 0;
+  int tokens = 0;              // per sequence
+  long long rows = 0;          // batch * tokens
+  int n_axes = 0;
+  int n_pairs = 0;             // 0: no rotation
+  int inverse = 0;
+  int split_heads = 0;         // set by the launcher
+  const float* pos = nullptr;  // [(batch,) tokens, n_axes]
+  long long pos_batch = 0;
+  const float* q_gain = nullptr;
+  const float* k_gain = nullptr;
+  float eps = 0.f;
+  float* part = nullptr;       // backward: a row [2][head_dim] per block
+  float* dq_gain = nullptr;
+  float* dk_gain = nullptr;
+  uint8_t axis[128] = {};
+  double turns[128] = {};      // revolutions per unit of position
+};
+
+// Blocks an SM gets at most (their warps stride over the tokens).  The backward pass writes
+// a row of the workspace per block.
+constexpr int kHeadRowsPerSm = 16;
+constexpr int kHeadRowsBwdPerSm = 5;
+constexpr size_t head_rows_bwd_bytes(int head_dim) {
+  return size_t(kHeadRowsBwdPerSm) * kMaxSkCtas * 2 * head_dim * sizeof(float);
+}
+
+// dtype 0 bf16, 1 fp16, 2 fp32; mode 0 rotation of in[0], 1 norm + rotation, 2 its backward.
+int launch_head_rows(const DevCtx& ctx, int dtype, int mode, HeadRows a, bool halves,
+                     cudaStream_t stream);
+
 // ---------------------------------------------------------------- row kernels
 int launch_ln_modulate(const bf16* x, int n, int d, float eps, const float* shift,
                        const float* scale, bf16* h, cudaStream_t stream);

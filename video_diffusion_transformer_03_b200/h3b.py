@@ -59,8 +59,22 @@ class Int8Block(ctypes.Structure):
                 ("w_qkv_q", "s_qkv", "w_fc1_q", "s_fc1", "w_fc2_q", "s_fc2")]
 
 
+class HeadView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong), ("head_stride", ctypes.c_longlong)]
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("magic", ctypes.c_uint), ("n_axes", ctypes.c_int), ("n_pairs", ctypes.c_int),
+                ("pairing", ctypes.c_int), ("axis", ctypes.c_ubyte * 128),
+                ("turns", ctypes.c_double * 128)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_V = ctypes.POINTER(HeadView)
+_R = ctypes.POINTER(RopePlan)
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 
@@ -122,6 +136,12 @@ _SIGS = {
                               _P, _P, _P, _P, _SZ, _P]),
     "h3b_attention": (_I, [_P, _I, _I, _I, _P, _P, _SZ, _P]),
     "h3b_layer_mask": (_I, [_P, _I, _I, _I, _P]),
+    "h3b_rope_plan_make": (_I, [_I, ctypes.POINTER(ctypes.c_int), _F, _I, _I, _R]),
+    "h3b_rope_axes": (_I, [_R, _I, _V, _I, _I, _I, _I, _P, _L, _I, _V, _P]),
+    "h3b_qk_norm_rope": (_I, [_R, _I, _V, _V, _I, _I, _I, _I, _I, _P, _P, _F, _P, _L, _V, _V, _P]),
+    "h3b_qk_norm_rope_backward_workspace_size": (_SZ, [_I]),
+    "h3b_qk_norm_rope_backward": (_I, [_R, _I, _V, _V, _I, _I, _I, _I, _I, _P, _P, _F, _P, _L, _V,
+                                       _V, _V, _V, _P, _P, _P, _SZ, _P]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -617,6 +637,140 @@ def attention(qkv, n_heads, head_dim, out, ws=None, stream=None) -> None:
     wp, wb = _wsargs(ws)
     _check(lib.h3b_attention(_ptr(qkv), qkv.shape[0], n_heads, head_dim, _ptr(out), wp, wb,
                              _stream(stream)))
+
+
+# ---------------------------------------------------------------------- operators on heads
+ROPE_ADJACENT, ROPE_HALVES = 0, 1
+DT_BF16, DT_F16, DT_F32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
+
+
+def _heads(t, name: str, ref=None, heads=None) -> HeadView:
+    """The view of a [batch, tokens, heads, head_dim] or [tokens, heads, head_dim] tensor;
+    ref: a tensor whose sizes (heads apart, if given), type and device it must share."""
+    if not t.is_cuda or t.dim() not in (3, 4):
+        raise TypeError(f"{name}: expected a CUDA tensor [batch, tokens, heads, head_dim] or "
+                        f"[tokens, heads, head_dim], got {t.device} {tuple(t.shape)}")
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous")
+    if ref is not None:
+        want = ref.shape if heads is None else ref.shape[:-2] + (heads, ref.shape[-1])
+        if t.shape != want or t.dtype != ref.dtype or t.device != ref.device:
+            raise ValueError(f"{name}: expected {tuple(want)} {ref.dtype} on {ref.device}, got "
+                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    elif t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return HeadView(t.data_ptr(), s[0] if t.dim() == 4 else 0, s[-3], s[-2])
+
+
+def _dtype(t, name: str) -> int:
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise TypeError(f"{name}: {t.dtype} is not bf16, fp16 or fp32") from None
+
+
+def _vector(t, name: str, ref, n: int):
+    """Data pointer of an optional contiguous fp32 vector of n elements on ref's device."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.device != ref.device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous fp32 values on {ref.device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _positions(plan, pos, ref):
+    """(pointer, batch stride) of pos [tokens, axes] or [batch, tokens, axes] fp32."""
+    if plan is None:
+        return None, 0
+    if pos is None:
+        raise ValueError("pos: a plan needs positions")
+    want = ref.shape[:-2] + (plan.n_axes,)
+    if (pos.dtype != torch.float32 or pos.device != ref.device
+            or pos.shape not in (want, want[-2:])):
+        raise ValueError(f"pos: expected {tuple(want)} or {tuple(want[-2:])} fp32 on {ref.device}, "
+                         f"got {tuple(pos.shape)} {pos.dtype} on {pos.device}")
+    if not pos[0].is_contiguous() if pos.dim() == 3 and len(pos) else not pos.is_contiguous():
+        raise ValueError("pos must be contiguous")
+    return pos.data_ptr(), pos.stride(0) if pos.dim() == 3 else 0
+
+
+def make_rope_axes(split: Sequence[int], theta: float = 10000.0, pairing: int = ROPE_ADJACENT,
+                   shared_freq: bool = False) -> RopePlan:
+    """Rotary positions with len(split) axes, axis a on split[a] channels of every head, in
+    order (h3b_rope_plan_make).  shared_freq: one frequency ladder over all axes."""
+    plan = RopePlan()
+    arr = (ctypes.c_int * max(len(split), 1))(*split)
+    _check(lib.h3b_rope_plan_make(len(split), arr, theta, pairing, int(bool(shared_freq)),
+                                  ctypes.byref(plan)))
+    return plan
+
+
+def _sizes(t):
+    return (t.shape[0] if t.dim() == 4 else 1), t.shape[-3], t.shape[-2], t.shape[-1]
+
+
+def rope_axes(plan: RopePlan, x, pos, out, inverse: bool = False, stream=None) -> None:
+    """out = x [(batch,) tokens, heads, head_dim] (bf16, fp16 or fp32; any strides with
+    head_dim contiguous) rotated at pos [(batch,) tokens, axes] fp32.  inverse: turned back,
+    which is the gradient of the rotation.  out may be x."""
+    vx = _heads(x, "x")
+    vo = _heads(out, "out", x)
+    batch, tokens, heads, head_dim = _sizes(x)
+    pp, ps = _positions(plan, pos, x)
+    _check(lib.h3b_rope_axes(plan, _dtype(x, "x"), vx, batch, tokens, heads, head_dim, pp, ps,
+                             int(bool(inverse)), vo, _stream(stream)))
+
+
+def qk_norm_rope(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos, q_out, k_out,
+                 stream=None) -> None:
+    """RMS norm of every head of q and k (gains [head_dim] fp32 or None), then the rotation
+    of rope_axes (plan None: none).  k may have fewer heads than q, or be None."""
+    vq = _heads(q, "q")
+    vqo = _heads(q_out, "q_out", q)
+    batch, tokens, heads, head_dim = _sizes(q)
+    kv_heads, vk, vko = 0, None, None
+    if k is not None:
+        kv_heads = k.shape[-2]
+        vk = _heads(k, "k", q, kv_heads)
+        vko = _heads(k_out, "k_out", k)
+    pp, ps = _positions(plan, pos, q)
+    _check(lib.h3b_qk_norm_rope(plan, _dtype(q, "q"), vq, vk, batch, tokens, heads, kv_heads,
+                                head_dim, _vector(q_gain, "q_gain", q, head_dim),
+                                _vector(k_gain, "k_gain", q, head_dim), eps, pp, ps, vqo, vko,
+                                _stream(stream)))
+
+
+def qk_norm_rope_backward_workspace_size(head_dim: int) -> int:
+    n = int(lib.h3b_qk_norm_rope_backward_workspace_size(head_dim))
+    if n == 0:
+        _check(H3B_EINVAL)
+    return n
+
+
+def qk_norm_rope_backward(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos, g_q,
+                          g_k, dq, dk, dq_gain, dk_gain, ws, stream=None) -> None:
+    """Gradients of qk_norm_rope: from its inputs and the gradients g_q, g_k of its outputs to
+    dq, dk (may be g_q, g_k) and dq_gain, dk_gain [head_dim] fp32 (None: not wanted)."""
+    vq = _heads(q, "q")
+    vgq = _heads(g_q, "g_q", q)
+    vdq = _heads(dq, "dq", q)
+    batch, tokens, heads, head_dim = _sizes(q)
+    kv_heads, vk, vgk, vdk = 0, None, None, None
+    if k is not None:
+        kv_heads = k.shape[-2]
+        vk = _heads(k, "k", q, kv_heads)
+        vgk = _heads(g_k, "g_k", k)
+        vdk = _heads(dk, "dk", k)
+    pp, ps = _positions(plan, pos, q)
+    wp, wb = _wsargs(ws)
+    _check(lib.h3b_qk_norm_rope_backward(
+        plan, _dtype(q, "q"), vq, vk, batch, tokens, heads, kv_heads, head_dim,
+        _vector(q_gain, "q_gain", q, head_dim), _vector(k_gain, "k_gain", q, head_dim), eps, pp,
+        ps, vgq, vgk, vdq, vdk, _vector(dq_gain, "dq_gain", q, head_dim),
+        _vector(dk_gain, "dk_gain", q, head_dim), wp, wb, _stream(stream)))
 
 
 def layer_mask(mods_host: np.ndarray, n_active: int) -> np.ndarray:
