@@ -205,6 +205,8 @@ int head_rows_common(const char* who, const h3b_rope_plan* plan, int dtype, int 
                      tokens, q_heads, k_heads);
   if (head_dim < 8 || head_dim > 256 || head_dim % 8)
     return set_error(H3B_EINVAL, "%s: head_dim %d must be a multiple of 8 in 8..256", who, head_dim);
+  if (1ll * batch * tokens > (1ll << 30))
+    return set_error(H3B_EINVAL, "%s: too many tokens (%d sequences of %d)", who, batch, tokens);
   a->tokens = tokens;
   a->rows = 1ll * batch * tokens;
   a->heads[0] = q_heads;

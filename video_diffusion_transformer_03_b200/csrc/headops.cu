@@ -12,11 +12,12 @@
 // Everything between the load and the store is in 32 bits; one rounding, at the store.
 //
 // What bounds it: HBM.  Forward reads and writes every head once, backward reads x and gy
-// and writes dx.  So a warp takes a token and walks over its heads: each lane owns eight
+// and writes dx.  So a warp takes a token and walks over its heads of q or of k (a block has
+// one or the other, which keeps one set of gains and sums in registers): each lane owns eight
 // channels of a head (the four pairs 4 s .. 4 s + 3 of its slot s, in both pairings), so the
 // angles of a token are computed once for all heads of the warp's item, pairs never cross
-// lanes, and the only shuffles are those of the norm's sum.  Loads of kPass groups of heads
-// are issued before the first use.
+// lanes, and the only shuffles are those of the norm's sums.  An item's first loads are issued
+// before its angles are computed, later ones while the heads before them are worked on.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -136,13 +137,25 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Item = one token, or one chunk of kPass * (32 / LPH) heads of it where tokens are few
-// (split_heads).  Chunks hold heads of q or of k, never both.
+// A group is kPass passes of 32 / LPH heads.  An item is one token, or (parts > 1, where
+// tokens are few) an equal share of its groups.
+template <typename T, int MODE>
+constexpr int pass_count() {
+  return (MODE == kModeNormBwd || sizeof(T) == 4) ? 1 : 2;
+}
+
+// Blocks that are on an SM at a time (their registers: 64, 80 and 128 a thread); the grid is
+// that many a SM at most.
+constexpr int blocks_per_sm(int mode) {
+  return mode == kModeNormBwd ? kHeadRowsBwdPerSm : mode == kModeNorm ? 6 : 8;
+}
+
 template <typename T, bool HALVES, int LPH, int MODE>
-__global__ void __launch_bounds__(kWarps * 32) k_head_rows(const __grid_constant__ HeadRows a) {
-  constexpr int kPass = (MODE == kModeNormBwd || sizeof(T) == 4) ? 2 : 4;
-  constexpr int kHeads = 32 / LPH;           // heads of one pass
-  constexpr int kChunk = kPass * kHeads;     // heads of a chunk
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(const __grid_constant__ HeadRows a) {
+  constexpr int kPass = pass_count<T, MODE>();
+  constexpr int kHeads = 32 / LPH;
+  constexpr int kGroup = kPass * kHeads;
+  constexpr bool kBwd = MODE == kModeNormBwd;
   const int lane = threadIdx.x & 31;
   const int slot = lane % LPH, sub = lane / LPH;
   const bool live = slot * 8 < a.head_dim;
@@ -151,105 +164,118 @@ __global__ void __launch_bounds__(kWarps * 32) k_head_rows(const __grid_constant
   const int c0 = half_slot ? slot * 4 : slot * 8;
   const int c1 = half_slot ? a.n_pairs + slot * 4 : slot * 8 + 4;
 
-  double turns[4];
-  int axis[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int p = slot * 4 + i;
-    const bool in = p < a.n_pairs;
-    turns[i] = in ? a.turns[in ? p : 0] : 0.0;
-    axis[i] = in ? a.axis[in ? p : 0] : 0;
-  }
-  float gain[2][8];
-  float acc[2][8];
-#pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      acc[w][i] = 0.f;
-      gain[w][i] = 1.f;
-      if constexpr (MODE != kModeRope) {
-        const float* g = w ? a.k_gain : a.q_gain;
-        if (g != nullptr && live) gain[w][i] = __ldg(g + (i < 4 ? c0 + i : c1 + i - 4));
-      }
-    }
-  const float inv_hd = 1.0f / static_cast<float>(a.head_dim);
+  const int w = static_cast<int>(blockIdx.x) >= a.q_blocks;
+  const unsigned block = w ? blockIdx.x - a.q_blocks : blockIdx.x;
+  const unsigned blocks = w ? gridDim.x - a.q_blocks : static_cast<unsigned>(a.q_blocks);
+  const HeadView in = a.in[w], out = a.out[w];
+  const int heads = a.heads[w], parts = a.parts[w];
+  const int groups = (heads + kGroup - 1) / kGroup;
+  const unsigned n_items = static_cast<unsigned>(a.rows) * parts;
 
-  const int q_chunks = (a.heads[0] + kChunk - 1) / kChunk;
-  const int k_chunks = (a.heads[1] + kChunk - 1) / kChunk;
-  const int chunks = q_chunks + k_chunks;
-  const long long n_items = a.split_heads ? a.rows * chunks : a.rows;
-  const long long stride = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-       item < n_items; item += stride) {
-    const long long row = a.split_heads ? item / chunks : item;
-    const int first = a.split_heads ? static_cast<int>(item - row * chunks) : 0;
-    const int last = a.split_heads ? first + 1 : chunks;
-    const long long b = row / a.tokens, t = row - b * a.tokens;
-    float cs[4], sn[4];
-    if (a.n_pairs > 0) {
-      const float* pos = a.pos + b * a.pos_batch + t * a.n_axes;
+  double turns[4] = {0.0, 0.0, 0.0, 0.0};
+  uint32_t axes = 0;
+  float gain[8];
+  float acc[8];
+  bool have_lane = false;
+  const float inv_hd = 1.0f / static_cast<float>(a.head_dim);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-        if (slot * 4 + i < a.n_pairs)
-          sincos_turns(static_cast<double>(__ldg(pos + axis[i])) * turns[i], sn[i], cs[i]);
-        if (MODE == kModeNormBwd || (MODE == kModeRope && a.inverse)) sn[i] = -sn[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cs[i] = 1.f;
-        sn[i] = 0.f;
-      }
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+
+  for (unsigned item = block * kWarps + (threadIdx.x >> 5); item < n_items;
+       item += blocks * kWarps) {
+    unsigned row = item, b = 0;
+    int g0 = 0, g1 = groups;
+    if (parts > 1) {
+      row = item / parts;
+      const int part = static_cast<int>(item - row * parts);
+      g0 = groups * part / parts;
+      g1 = groups * (part + 1) / parts;
     }
-    for (int ch = first; ch < last; ++ch) {
-      const int w = ch >= q_chunks;
-      const int h0 = (w ? ch - q_chunks : ch) * kChunk + sub;
-      const HeadView& in = a.in[w];
-      const HeadView& out = a.out[w];
-      const T* src = static_cast<const T*>(in.data) + b * in.batch + t * in.token;
-      T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token;
-      Raw<T> x[kPass], gy[kPass];
+    unsigned t = row;
+    if (a.rows != a.tokens) {
+      b = row / static_cast<unsigned>(a.tokens);
+      t = row - b * static_cast<unsigned>(a.tokens);
+    }
+    const T* src = static_cast<const T*>(in.data) + b * in.batch + t * in.token;
+    const T* grd = nullptr;
+    if constexpr (kBwd)
+      grd = static_cast<const T*>(a.grad[w].data) + b * a.grad[w].batch + t * a.grad[w].token;
+    T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token;
+
+    Raw<T> x[kPass], gy[kPass];
+    auto load = [&](int g) {
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        const int h = h0 + i * kHeads;
-        const bool on = live && h < a.heads[w];
+        const int h = g * kGroup + i * kHeads + sub;
+        const bool on = live && h < heads;
         x[i] = Raw<T>{};
         if (on) load_raw<T, HALVES>(src + h * in.head, c0, c1, x[i]);
-        if constexpr (MODE == kModeNormBwd) {
-          const HeadView& gv = a.grad[w];
-          const T* g = static_cast<const T*>(gv.data) + b * gv.batch + t * gv.token;
+        if constexpr (kBwd) {
           gy[i] = Raw<T>{};
-          if (on) load_raw<T, HALVES>(g + h * gv.head, c0, c1, gy[i]);
+          if (on) load_raw<T, HALVES>(grd + h * a.grad[w].head, c0, c1, gy[i]);
         }
       }
+    };
+    load(g0);
+    if (!have_lane) {
+      // this lane's constants, behind its first loads
+      have_lane = true;
+      if (turned) {
+        const double2 t0 = *reinterpret_cast<const double2*>(a.turns + slot * 4);
+        const double2 t1 = *reinterpret_cast<const double2*>(a.turns + slot * 4 + 2);
+        turns[0] = t0.x; turns[1] = t0.y; turns[2] = t1.x; turns[3] = t1.y;
+        axes = *reinterpret_cast<const uint32_t*>(a.axis + slot * 4);
+      }
+      if constexpr (MODE != kModeRope) {
+        const float* g = w ? a.k_gain : a.q_gain;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          gain[i] = (g != nullptr && live) ? __ldg(g + (i < 4 ? c0 + i : c1 + i - 4)) : 1.f;
+      }
+    }
+    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+    if (turned) {
+      // pairs past the rotated width have turns 0: they stay
+      const float* pos = a.pos + b * a.pos_batch + static_cast<size_t>(t) * a.n_axes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (slot * 4 + i < a.n_pairs)
+          sincos_turns(static_cast<double>(__ldg(pos + ((axes >> (8 * i)) & 0xffu))) * turns[i],
+                       sn[i], cs[i]);
+        if (kBwd || (MODE == kModeRope && a.inverse)) sn[i] = -sn[i];
+      }
+    }
+    for (int g = g0; g < g1; ++g) {
+      Raw<T> xc[kPass], gc[kPass];
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        const int h = h0 + i * kHeads;
+        xc[i] = x[i];
+        if constexpr (kBwd) gc[i] = gy[i];
+      }
+      if (g + 1 < g1) load(g + 1);
+#pragma unroll
+      for (int i = 0; i < kPass; ++i) {
+        const int h = g * kGroup + i * kHeads + sub;
         float f[8];
-        widen<T>(x[i], f);
+        widen<T>(xc[i], f);
         if constexpr (MODE != kModeRope) {
           float ss = 0.f;
 #pragma unroll
           for (int c = 0; c < 8; ++c) ss = fmaf(f[c], f[c], ss);
           const float rstd = rsqrtf(head_sum<LPH>(ss) * inv_hd + a.eps);
-          if constexpr (MODE == kModeNorm) {
+          if constexpr (!kBwd) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] *= rstd * (w ? gain[1][c] : gain[0][c]);
+            for (int c = 0; c < 8; ++c) f[c] *= rstd * gain[c];
           } else {
             float z[8];
-            widen<T>(gy[i], z);
+            widen<T>(gc[i], z);
             rotate<HALVES>(z, cs, sn);
             float dot = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               f[c] *= rstd;
-              const float zn = z[c] * f[c];
-              if (w) acc[1][c] += zn;
-              else acc[0][c] += zn;
-              z[c] *= w ? gain[1][c] : gain[0][c];
+              acc[c] = fmaf(z[c], f[c], acc[c]);
+              z[c] *= gain[c];
               dot = fmaf(z[c], f[c], dot);
             }
             dot = head_sum<LPH>(dot) * inv_hd;
@@ -257,8 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32) k_head_rows(const __grid_constant
             for (int c = 0; c < 8; ++c) f[c] = rstd * fmaf(-f[c], dot, z[c]);
           }
         }
-        if constexpr (MODE != kModeNormBwd) rotate<HALVES>(f, cs, sn);
-        if (live && h < a.heads[w]) {
+        if constexpr (!kBwd) rotate<HALVES>(f, cs, sn);
+        if (live && h < heads) {
           Raw<T> y;
           narrow<T>(f, y);
           store_raw<T, HALVES>(dst + h * out.head, c0, c1, y);
@@ -266,71 +292,84 @@ __global__ void __launch_bounds__(kWarps * 32) k_head_rows(const __grid_constant
       }
     }
   }
-  if constexpr (MODE == kModeNormBwd) {
-    // the block's share of the gains' gradients: lanes of the same slot, then its warps in
-    // order, then one row [2][head_dim] of the workspace
-    __shared__ float red[kWarps][2][LPH * 8];
+  if constexpr (kBwd) {
+    // the block's share of the gain's gradient: lanes of the same slot, then its warps in
+    // order, then one row [head_dim] of the workspace
+    __shared__ float red[kWarps][LPH * 8];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
+    for (int c = 0; c < 8; ++c) {
+      float v = acc[c];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float v = acc[w][c];
-#pragma unroll
-        for (int o = LPH; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (sub == 0 && live) red[threadIdx.x >> 5][w][c < 4 ? c0 + c : c1 + c - 4] = v;
-      }
+      for (int o = LPH; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (sub == 0 && live) red[threadIdx.x >> 5][c < 4 ? c0 + c : c1 + c - 4] = v;
+    }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.head_dim; i += kWarps * 32) {
-      const int w = i >= a.head_dim, c = w ? i - a.head_dim : i;
+    for (int c = threadIdx.x; c < a.head_dim; c += kWarps * 32) {
       float v = 0.f;
 #pragma unroll
-      for (int j = 0; j < kWarps; ++j) v += red[j][w][c];
-      a.part[static_cast<size_t>(blockIdx.x) * 2 * a.head_dim + i] = v;
+      for (int j = 0; j < kWarps; ++j) v += red[j][c];
+      a.part[static_cast<size_t>(blockIdx.x) * a.head_dim + c] = v;
     }
   }
 }
 
-// Gains' gradients from the blocks' rows, in a fixed order: a block per 32 columns, warp j
-// takes rows j, j + 32, ..., then the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) k_gain_reduce(const float* __restrict__ part, int rows,
-                                                      int head_dim, float* __restrict__ dq_gain,
+// Gains' gradients from the blocks' rows, in a fixed order: a block per 32 columns of one
+// gain (blockIdx.y: q or k), warp j takes rows j, j + 32, ..., then the 32 sums are added.
+__global__ void __launch_bounds__(1024) k_gain_reduce(const float* __restrict__ part, int q_rows,
+                                                      int k_rows, int head_dim,
+                                                      float* __restrict__ dq_gain,
                                                       float* __restrict__ dk_gain) {
-  __shared__ float red[32][32];
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
+  const int rows = blockIdx.y ? k_rows : q_rows;
+  if (blockIdx.y) part += static_cast<size_t>(q_rows) * head_dim;
+  float* out = blockIdx.y ? dk_gain : dq_gain;
+  if (out == nullptr) return;
   float v = 0.f;
-  if (col < 2 * head_dim)
-    for (int r = warp; r < rows; r += 32) v += part[static_cast<size_t>(r) * 2 * head_dim + col];
+  if (col < head_dim)
+#pragma unroll 4
+    for (int r = warp; r < rows; r += 32) v += part[static_cast<size_t>(r) * head_dim + col];
   red[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && col < 2 * head_dim) {
+  v = red[lane][warp];  // warp c adds the 32 sums of column c
 #pragma unroll
-    for (int j = 1; j < 32; ++j) v += red[j][lane];
-    float* out = col < head_dim ? dq_gain : dk_gain;
-    if (out != nullptr) out[col < head_dim ? col : col - head_dim] = v;
-  }
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (lane == 0 && blockIdx.x * 32 + warp < head_dim) out[blockIdx.x * 32 + warp] = v;
 }
 
 template <typename T, bool HALVES, int LPH, int MODE>
 int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
-  constexpr int kPass = (MODE == kModeNormBwd || sizeof(T) == 4) ? 2 : 4;
-  constexpr int kChunk = kPass * (32 / LPH);
-  const int chunks = (a.heads[0] + kChunk - 1) / kChunk + (a.heads[1] + kChunk - 1) / kChunk;
-  // Tokens alone keep every SM's warps busy from 16 a SM on; with fewer a token's heads are
-  // dealt to several warps, each of which computes the token's angles again.
-  a.split_heads = a.rows < 16ll * ctx.num_sms;
-  const long long items = a.split_heads ? a.rows * chunks : a.rows;
-  const long long most = 1ll * (MODE == kModeNormBwd ? kHeadRowsBwdPerSm : kHeadRowsPerSm) *
-                         std::min(ctx.num_sms, kMaxSkCtas);
-  const long long blocks = std::min<long long>((items + kWarps - 1) / kWarps, most);
-  if (blocks > 0) {
+  constexpr int kGroup = pass_count<T, MODE>() * (32 / LPH);
+  const int sms = std::min(ctx.num_sms, kMaxSkCtas);
+  const long long most = 1ll * blocks_per_sm(MODE) * sms;
+  // Tokens alone keep an SM busy from about 24 of its warps on; with fewer, a token's groups
+  // of heads are dealt to several warps, each of which computes the token's angles again.
+  long long items[2], total = 0;
+  for (int w = 0; w < 2; ++w) {
+    const int groups = (a.heads[w] + kGroup - 1) / kGroup;
+    const long long want = a.rows > 0 ? (24ll * sms + a.rows - 1) / a.rows : 1;
+    a.parts[w] = static_cast<int>(std::max<long long>(1, std::min<long long>(groups, want)));
+    items[w] = groups > 0 ? a.rows * a.parts[w] : 0;
+    total += items[w] * groups / a.parts[w];
+  }
+  // q's share of the blocks is its share of the work
+  long long blocks[2];
+  for (int w = 0; w < 2; ++w) {
+    const int groups = (a.heads[w] + kGroup - 1) / kGroup;
+    const long long share = total > 0 ? (most * items[w] * groups / a.parts[w]) / total : 0;
+    blocks[w] = std::min<long long>((items[w] + kWarps - 1) / kWarps, std::max<long long>(share, 1));
+  }
+  a.q_blocks = static_cast<int>(blocks[0]);
+  if (blocks[0] + blocks[1] > 0) {
     k_head_rows<T, HALVES, LPH, MODE>
-        <<<static_cast<unsigned>(blocks), kWarps * 32, 0, stream>>>(a);
+        <<<static_cast<unsigned>(blocks[0] + blocks[1]), kWarps * 32, 0, stream>>>(a);
     if (int rc = check_launch("head rows")) return rc;
   }
-  if (MODE != kModeNormBwd) return 0;
-  k_gain_reduce<<<(2 * a.head_dim + 31) / 32, 1024, 0, stream>>>(
-      a.part, static_cast<int>(blocks), a.head_dim, a.dq_gain, a.dk_gain);
+  if (MODE != kModeNormBwd || (!a.dq_gain && !a.dk_gain)) return 0;
+  k_gain_reduce<<<dim3((a.head_dim + 31) / 32, 2), 1024, 0, stream>>>(
+      a.part, static_cast<int>(blocks[0]), static_cast<int>(blocks[1]), a.head_dim, a.dq_gain,
+      a.dk_gain);
   return check_launch("gain reduce");
 }
 

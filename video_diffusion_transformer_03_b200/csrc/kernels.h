@@ -168,25 +168,25 @@ struct HeadRows {
   int n_axes = 0;
   int n_pairs = 0;             // 0: no rotation
   int inverse = 0;
-  int split_heads = 0;         // set by the launcher
+  int parts[2] = {1, 1};       // set by the launcher: warps that share a token's heads,
+  int q_blocks = 0;            // and the blocks that work on q
   const float* pos = nullptr;  // [(batch,) tokens, n_axes]
   long long pos_batch = 0;
   const float* q_gain = nullptr;
   const float* k_gain = nullptr;
   float eps = 0.f;
-  float* part = nullptr;       // backward: a row [2][head_dim] per block
+  float* part = nullptr;       // backward: a row [head_dim] per block
   float* dq_gain = nullptr;
   float* dk_gain = nullptr;
-  uint8_t axis[128] = {};
-  double turns[128] = {};      // revolutions per unit of position
+  alignas(16) uint8_t axis[128] = {};
+  alignas(16) double turns[128] = {};      // revolutions per unit of position
 };
 
-// Blocks an SM gets at most (their warps stride over the tokens).  The backward pass writes
-// a row of the workspace per block.
-constexpr int kHeadRowsPerSm = 16;
-constexpr int kHeadRowsBwdPerSm = 5;
+// Blocks of the backward pass on an SM; each writes a row of the workspace.
+constexpr int kHeadRowsBwdPerSm = 4;
 constexpr size_t head_rows_bwd_bytes(int head_dim) {
-  return size_t(kHeadRowsBwdPerSm) * kMaxSkCtas * 2 * head_dim * sizeof(float);
+  // one block more than the cap: q and k get at least one each
+  return (size_t(kHeadRowsBwdPerSm) * kMaxSkCtas + 1) * head_dim * sizeof(float);
 }
 
 // dtype 0 bf16, 1 fp16, 2 fp32; mode 0 rotation of in[0], 1 norm + rotation, 2 its backward.

@@ -645,56 +645,64 @@ DT_BF16, DT_F16, DT_F32 = 0, 1, 2
 _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
 
 
-def _heads(t, name: str, ref=None, heads=None) -> HeadView:
-    """The view of a [batch, tokens, heads, head_dim] or [tokens, heads, head_dim] tensor;
-    ref: a tensor whose sizes (heads apart, if given), type and device it must share."""
-    if not t.is_cuda or t.dim() not in (3, 4):
+def _lead(t, name: str):
+    """Shape, element type and device of a call's first tensor [(batch,) tokens, heads,
+    head_dim], which the others have to agree with."""
+    shape = t.shape
+    if not t.is_cuda or len(shape) not in (3, 4):
         raise TypeError(f"{name}: expected a CUDA tensor [batch, tokens, heads, head_dim] or "
-                        f"[tokens, heads, head_dim], got {t.device} {tuple(t.shape)}")
-    s = t.stride()
-    if s[-1] != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name}: head_dim must be contiguous")
-    if ref is not None:
-        want = ref.shape if heads is None else ref.shape[:-2] + (heads, ref.shape[-1])
-        if t.shape != want or t.dtype != ref.dtype or t.device != ref.device:
-            raise ValueError(f"{name}: expected {tuple(want)} {ref.dtype} on {ref.device}, got "
-                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
-    elif t.get_device() != torch.cuda.current_device():
+                        f"[tokens, heads, head_dim], got {t.device} {tuple(shape)}")
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return HeadView(t.data_ptr(), s[0] if t.dim() == 4 else 0, s[-3], s[-2])
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name}: {t.dtype} is not bf16, fp16 or fp32")
+    return shape, t.dtype, t.device
 
 
-def _dtype(t, name: str) -> int:
-    try:
-        return _DTYPES[t.dtype]
-    except KeyError:
-        raise TypeError(f"{name}: {t.dtype} is not bf16, fp16 or fp32") from None
+def _heads(t, name: str, shape, dtype, device) -> HeadView:
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    s = t.stride()
+    if s[-1] != 1 and shape[-1] != 1:
+        raise ValueError(f"{name}: head_dim must be contiguous")
+    return HeadView(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
 
 
-def _vector(t, name: str, ref, n: int):
-    """Data pointer of an optional contiguous fp32 vector of n elements on ref's device."""
+def _vector(t, name: str, n: int, device, dtype=torch.float32):
+    """Data pointer of an optional contiguous vector of n elements."""
     if t is None:
         return None
-    if t.dtype != torch.float32 or t.device != ref.device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous fp32 values on {ref.device}, got "
+    if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on {device}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _positions(plan, pos, ref):
+def _positions(plan, pos, shape, device):
     """(pointer, batch stride) of pos [tokens, axes] or [batch, tokens, axes] fp32."""
     if plan is None:
         return None, 0
     if pos is None:
         raise ValueError("pos: a plan needs positions")
-    want = ref.shape[:-2] + (plan.n_axes,)
-    if (pos.dtype != torch.float32 or pos.device != ref.device
-            or pos.shape not in (want, want[-2:])):
-        raise ValueError(f"pos: expected {tuple(want)} or {tuple(want[-2:])} fp32 on {ref.device}, "
-                         f"got {tuple(pos.shape)} {pos.dtype} on {pos.device}")
-    if not pos[0].is_contiguous() if pos.dim() == 3 and len(pos) else not pos.is_contiguous():
-        raise ValueError("pos must be contiguous")
-    return pos.data_ptr(), pos.stride(0) if pos.dim() == 3 else 0
+    ps = pos.shape
+    one = len(ps) == 2
+    if ((ps[-2:] != (shape[-3], plan.n_axes) if len(ps) >= 2 else True)
+            or not (one or (len(ps) == 3 and len(shape) == 4 and ps[0] == shape[0]))
+            or pos.dtype is not torch.float32 or pos.device != device):
+        raise ValueError(f"pos: expected [tokens, {plan.n_axes}] or [batch, tokens, {plan.n_axes}] "
+                         f"fp32 on {device} for {tuple(shape)}, got {tuple(ps)} {pos.dtype} on "
+                         f"{pos.device}")
+    s = pos.stride()
+    if (s[-1] != 1 and ps[-1] > 1) or (s[-2] != ps[-1] and ps[-2] > 1):
+        raise ValueError("pos: the positions of a sequence must be contiguous")
+    return pos.data_ptr(), 0 if one else s[0]
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def make_rope_axes(split: Sequence[int], theta: float = 10000.0, pairing: int = ROPE_ADJACENT,
@@ -708,39 +716,41 @@ def make_rope_axes(split: Sequence[int], theta: float = 10000.0, pairing: int = 
     return plan
 
 
-def _sizes(t):
-    return (t.shape[0] if t.dim() == 4 else 1), t.shape[-3], t.shape[-2], t.shape[-1]
-
-
 def rope_axes(plan: RopePlan, x, pos, out, inverse: bool = False, stream=None) -> None:
     """out = x [(batch,) tokens, heads, head_dim] (bf16, fp16 or fp32; any strides with
     head_dim contiguous) rotated at pos [(batch,) tokens, axes] fp32.  inverse: turned back,
     which is the gradient of the rotation.  out may be x."""
-    vx = _heads(x, "x")
-    vo = _heads(out, "out", x)
-    batch, tokens, heads, head_dim = _sizes(x)
-    pp, ps = _positions(plan, pos, x)
-    _check(lib.h3b_rope_axes(plan, _dtype(x, "x"), vx, batch, tokens, heads, head_dim, pp, ps,
-                             int(bool(inverse)), vo, _stream(stream)))
+    shape, dtype, device = _lead(x, "x")
+    pp, ps = _positions(plan, pos, shape, device)
+    _check(lib.h3b_rope_axes(plan, _DTYPES[dtype], _heads(x, "x", shape, dtype, device),
+                             shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], shape[-1],
+                             pp, ps, 1 if inverse else 0, _heads(out, "out", shape, dtype, device),
+                             _raw_stream(stream, device)))
+
+
+def _k_shape(shape, k):
+    """Shape of k (its own number of heads) and that number; 0 heads without k."""
+    if k is None:
+        return None, 0
+    return shape[:-2] + (k.shape[-2], shape[-1]), k.shape[-2]
 
 
 def qk_norm_rope(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos, q_out, k_out,
                  stream=None) -> None:
     """RMS norm of every head of q and k (gains [head_dim] fp32 or None), then the rotation
     of rope_axes (plan None: none).  k may have fewer heads than q, or be None."""
-    vq = _heads(q, "q")
-    vqo = _heads(q_out, "q_out", q)
-    batch, tokens, heads, head_dim = _sizes(q)
-    kv_heads, vk, vko = 0, None, None
-    if k is not None:
-        kv_heads = k.shape[-2]
-        vk = _heads(k, "k", q, kv_heads)
-        vko = _heads(k_out, "k_out", k)
-    pp, ps = _positions(plan, pos, q)
-    _check(lib.h3b_qk_norm_rope(plan, _dtype(q, "q"), vq, vk, batch, tokens, heads, kv_heads,
-                                head_dim, _vector(q_gain, "q_gain", q, head_dim),
-                                _vector(k_gain, "k_gain", q, head_dim), eps, pp, ps, vqo, vko,
-                                _stream(stream)))
+    shape, dtype, device = _lead(q, "q")
+    hd = shape[-1]
+    pp, ps = _positions(plan, pos, shape, device)
+    ks, kv_heads = _k_shape(shape, k)
+    _check(lib.h3b_qk_norm_rope(
+        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, device),
+        None if k is None else _heads(k, "k", ks, dtype, device),
+        shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], kv_heads, hd,
+        _vector(q_gain, "q_gain", hd, device), _vector(k_gain, "k_gain", hd, device), eps, pp, ps,
+        _heads(q_out, "q_out", shape, dtype, device),
+        None if k is None else _heads(k_out, "k_out", ks, dtype, device),
+        _raw_stream(stream, device)))
 
 
 def qk_norm_rope_backward_workspace_size(head_dim: int) -> int:
@@ -754,23 +764,23 @@ def qk_norm_rope_backward(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: f
                           g_k, dq, dk, dq_gain, dk_gain, ws, stream=None) -> None:
     """Gradients of qk_norm_rope: from its inputs and the gradients g_q, g_k of its outputs to
     dq, dk (may be g_q, g_k) and dq_gain, dk_gain [head_dim] fp32 (None: not wanted)."""
-    vq = _heads(q, "q")
-    vgq = _heads(g_q, "g_q", q)
-    vdq = _heads(dq, "dq", q)
-    batch, tokens, heads, head_dim = _sizes(q)
-    kv_heads, vk, vgk, vdk = 0, None, None, None
-    if k is not None:
-        kv_heads = k.shape[-2]
-        vk = _heads(k, "k", q, kv_heads)
-        vgk = _heads(g_k, "g_k", k)
-        vdk = _heads(dk, "dk", k)
-    pp, ps = _positions(plan, pos, q)
+    shape, dtype, device = _lead(q, "q")
+    hd = shape[-1]
+    pp, ps = _positions(plan, pos, shape, device)
+    ks, kv_heads = _k_shape(shape, k)
     wp, wb = _wsargs(ws)
+
+    def kview(t, name):
+        return None if k is None else _heads(t, name, ks, dtype, device)
+
     _check(lib.h3b_qk_norm_rope_backward(
-        plan, _dtype(q, "q"), vq, vk, batch, tokens, heads, kv_heads, head_dim,
-        _vector(q_gain, "q_gain", q, head_dim), _vector(k_gain, "k_gain", q, head_dim), eps, pp,
-        ps, vgq, vgk, vdq, vdk, _vector(dq_gain, "dq_gain", q, head_dim),
-        _vector(dk_gain, "dk_gain", q, head_dim), wp, wb, _stream(stream)))
+        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, device), kview(k, "k"),
+        shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], kv_heads, hd,
+        _vector(q_gain, "q_gain", hd, device), _vector(k_gain, "k_gain", hd, device), eps, pp, ps,
+        _heads(g_q, "g_q", shape, dtype, device), kview(g_k, "g_k"),
+        _heads(dq, "dq", shape, dtype, device), kview(dk, "dk"),
+        _vector(dq_gain, "dq_gain", hd, device), _vector(dk_gain, "dk_gain", hd, device), wp, wb,
+        _raw_stream(stream, device)))
 
 
 def layer_mask(mods_host: np.ndarray, n_active: int) -> np.ndarray:
