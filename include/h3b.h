@@ -648,6 +648,35 @@ int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_he
                               const h3b_head_view* dk, float* dq_gain, float* dk_gain, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* Attention for a batch of sequences that share one long prefix:
+ *   out[b, i, h] = softmax over the keys that query i of sequence b sees, of
+ *                  scale * q[b, i, h] . key, times their values; key head h / (n_heads /
+ *                  n_kv_heads).
+ * The keys are the n_prefix shared ones (k_prefix, v_prefix [n_prefix, n_kv_heads, head_dim],
+ * one copy for the batch; batch_stride ignored) and the first kv_len[b] of the sequence's own
+ * (k, v [batch, n_kv, n_kv_heads, head_dim]).  causal == 0: all of them.  causal != 0: query
+ * i sees the prefix and own keys 0 .. i + kv_len[b] - q_len[b] (the queries are the sequence's
+ * last tokens).  A query that sees no key gets zeros.  Rows i >= q_len[b] of out are left as
+ * they were.
+ * q, out [batch, n_q, n_heads, head_dim]; dtype bf16 or fp16; head_dim 64 or 128; n_heads a
+ * multiple of n_kv_heads; n_prefix or n_kv may be 0, not both (their views are then ignored).
+ * No stride of q, k, v or the prefix may be 0 (dimensions of size 1 apart).
+ * kv_len, q_len: device int32 [batch], read by the kernels (a captured graph follows their
+ * values), clamped to [0, n_kv] and [0, n_q]; NULL: n_kv, n_q.  What lies in k, v behind
+ * kv_len[b] is never used, whatever it holds.  scale > 0, or 0 for 1 / sqrt(head_dim).
+ * Scores, softmax and sums are fp32; the weights are rounded to the type for the product with
+ * the values.  Equal calls give equal bits.
+ * ws: device scratch, 16-byte aligned, of h3b_attention_prefix_workspace_size bytes; one call
+ * at a time per buffer, nothing in it has to be zero.  out must not overlap the inputs. */
+size_t h3b_attention_prefix_workspace_size(int batch, int n_q, int n_heads, int n_kv_heads,
+                                           int head_dim, int n_prefix, int n_kv);
+int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view* k_prefix,
+                         const h3b_head_view* v_prefix, const h3b_head_view* k,
+                         const h3b_head_view* v, int batch, int n_q, int n_heads,
+                         int n_kv_heads, int head_dim, int n_prefix, int n_kv,
+                         const int32_t* kv_len, const int32_t* q_len, int causal, float scale,
+                         const h3b_head_view* out, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- host policy */
 /* Layer thinning mask (dothoosh.com "Aggressive optimisation levers": rank blocks by
  * their AdaLN gates, always keep the first and last block).  score_b = mean|gate_msa| +

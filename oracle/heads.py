@@ -65,8 +65,8 @@ def attention_prefix(q, kp, vp, k, v, kv_len=None, q_len=None, causal=False, sca
             vals = np.concatenate((vp[:, h // group], v[b, :nk, h // group]))
             s = q[b, :nq, h] @ keys.T * scale
             if causal:
-                last = len(kp) + nk - nq + np.arange(nq)
-                s = np.where(np.arange(len(keys))[None] <= last[:, None], s, -np.inf)
+                own = np.arange(len(keys))[None] - len(kp)      # negative: the prefix's
+                s = np.where(own <= np.maximum(nk - nq + np.arange(nq)[:, None], -1), s, -np.inf)
             top = s.max(-1, keepdims=True, initial=-np.inf)
             p = np.exp(s - np.where(np.isfinite(top), top, 0.0))
             total = p.sum(-1, keepdims=True)

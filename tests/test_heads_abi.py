@@ -129,7 +129,7 @@ def test_rope_axes_refusals():
     refused(rope(x=hv(ptr=P + 8)), "x is NULL or not 16-byte aligned")
     refused(rope(x=hv(t=516)), "x: stride 516")
     refused(rope(x=hv(h=-128)), "x: stride -128")
-    refused(rope(out=hv(b=0)), "out is an output and has stride 0")
+    refused(rope(out=hv(b=0)), "out has stride 0")
     refused(rope(dtype=2, out=hv(t=514)), "out: stride 514")
 
 
@@ -145,7 +145,7 @@ def test_qk_norm_rope_refusals():
     refused(norm(qg=P + 1), "gains")
     refused(norm(nk=-1), "sizes")
     refused(norm(k=hv(ptr=None)), "k is NULL")
-    refused(norm(qo=hv(h=0)), "q_out is an output")
+    refused(norm(qo=hv(h=0)), "q_out has stride 0")
     refused(norm(ko=hv(ptr=P + 4)), "k_out is NULL")
     refused(norm(plan=h3b.make_rope_axes((128,))), "pos")
 
@@ -158,10 +158,42 @@ def test_qk_norm_rope_backward_refusals():
                                            g or hv(), hv(), d or hv(), hv(), dqg, P, ws, nbytes, None)
 
     refused(back(g=hv(ptr=None)), "g_q is NULL")
-    refused(back(d=hv(t=0)), "dq is an output")
+    refused(back(d=hv(t=0)), "dq has stride 0")
     refused(back(dqg=P + 2), "gain gradient")
     for ws, nbytes in ((None, need), (P + 8, need), (P, need - 1)):
         assert back(ws=ws, nbytes=nbytes) == h3b.H3B_EWORKSPACE
     for hd in (0, 12, 264):
         with pytest.raises(h3b.H3BError, match="head_dim"):
             h3b.qk_norm_rope_backward_workspace_size(hd)
+
+
+def attend(dtype=0, q=None, kp=None, k=None, batch=2, nq=3, heads=4, kv=2, hd=64, prefix=16, nkv=8,
+           kv_len=None, q_len=None, scale=0.0, out=None, ws=P, nbytes=1 << 40):
+    return L.h3b_attention_prefix(dtype, q or hv(), kp or hv(), hv(), k or hv(), hv(), batch, nq, heads,
+                                  kv, hd, prefix, nkv, kv_len, q_len, 0, scale, out or hv(), ws, nbytes,
+                                  None)
+
+
+def test_attention_prefix_refusals():
+    refused(attend(dtype=2), "dtype")
+    refused(attend(dtype=7), "dtype")
+    for kw in (dict(batch=-1), dict(nq=-1), dict(prefix=-1), dict(nkv=-1), dict(batch=1 << 20)):
+        refused(attend(**kw), "sizes")
+    refused(attend(prefix=0, nkv=0), "no keys")
+    for kw in (dict(heads=3), dict(heads=0), dict(kv=0), dict(kv=8)):
+        refused(attend(**kw), "n_heads")
+    refused(attend(hd=96), "head_dim")
+    for s in (-0.5, float("nan"), float("inf")):
+        refused(attend(scale=s), "scale")
+    refused(attend(q=hv(ptr=None)), "q is NULL")
+    refused(attend(kp=hv(ptr=P + 2)), "k_prefix is NULL")
+    refused(attend(k=hv(t=0)), "k has stride 0")
+    refused(attend(k=hv(h=60)), "k: stride 60")
+    refused(attend(out=hv(b=0)), "out has stride 0")
+    refused(attend(kv_len=P + 1), "lengths")
+    refused(attend(q_len=P + 2), "lengths")
+    need = h3b.attention_prefix_workspace_size(2, 3, 4, 2, 64, 16, 8)
+    for ws, nbytes in ((None, need), (P + 8, need), (P, need - 1)):
+        assert attend(ws=ws, nbytes=nbytes) == h3b.H3B_EWORKSPACE
+    with pytest.raises(h3b.H3BError, match="n_heads"):
+        h3b.attention_prefix_workspace_size(2, 3, 4, 3, 64, 16, 8)

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libh3b.so")
-SOURCES = ["h3b_api.cu", "gemm_tc.cu", "attention_tc.cu", "rowops.cu", "headops.cu"]
+SOURCES = ["h3b_api.cu", "gemm_tc.cu", "attention_tc.cu", "rowops.cu", "headops.cu",
+           "attention_prefix.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                 "--expt-relaxed-constexpr", "-I", INCLUDE]

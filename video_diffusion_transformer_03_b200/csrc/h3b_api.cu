@@ -174,8 +174,9 @@ constexpr unsigned kRopePlanMagic = 0x68335250u;
 inline bool al4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // The caller's view as the kernels take it: strides of dimensions of size 1 become 0.
+// dense: other strides must not be 0 (an output, or what a TMA map describes).
 int head_view(const char* who, const char* name, const h3b_head_view* v, int dtype, int batch,
-              int tokens, int heads, bool output, HeadView* out) {
+              int tokens, int heads, bool dense, HeadView* out) {
   if (heads == 0 || tokens == 0 || batch == 0) return H3B_OK;
   if (!v || !v->data || !al16(v->data))
     return set_error(H3B_EINVAL, "%s: %s is NULL or not 16-byte aligned", who, name);
@@ -187,8 +188,8 @@ int head_view(const char* who, const char* name, const h3b_head_view* v, int dty
     if (st[i] < 0 || st[i] % unit || st[i] > (1ll << 38))
       return set_error(H3B_EINVAL, "%s: %s: stride %lld must be a non-negative multiple of 16 bytes",
                        who, name, st[i]);
-    if (output && size[i] > 1 && st[i] == 0)
-      return set_error(H3B_EINVAL, "%s: %s is an output and has stride 0", who, name);
+    if (dense && size[i] > 1 && st[i] == 0)
+      return set_error(H3B_EINVAL, "%s: %s has stride 0", who, name);
   }
   *out = HeadView{const_cast<void*>(v->data), st[0], st[1], st[2]};
   return H3B_OK;
@@ -233,6 +234,21 @@ int head_rows_common(const char* who, const h3b_rope_plan* plan, int dtype, int 
     a->axis[i] = plan->axis[i];
     a->turns[i] = plan->turns[i];
   }
+  return H3B_OK;
+}
+
+int prefix_sizes(int batch, int n_q, int heads, int kv_heads, int head_dim, int n_prefix, int n_kv) {
+  const char* who = "attention_prefix";
+  if (batch < 0 || n_q < 0 || n_prefix < 0 || n_kv < 0 || batch > 65535 || n_q > (1 << 24) ||
+      n_prefix > (1 << 28) || n_kv > (1 << 28))
+    return set_error(H3B_EINVAL, "%s: bad sizes (batch=%d queries=%d prefix=%d keys=%d)", who, batch,
+                     n_q, n_prefix, n_kv);
+  if (n_prefix == 0 && n_kv == 0) return set_error(H3B_EINVAL, "%s: no keys at all", who);
+  if (kv_heads <= 0 || heads <= 0 || heads % kv_heads || heads > 65536)
+    return set_error(H3B_EINVAL, "%s: n_heads=%d must be a multiple of n_kv_heads=%d", who, heads,
+                     kv_heads);
+  if (head_dim != 64 && head_dim != 128)
+    return set_error(H3B_EINVAL, "%s: head_dim %d must be 64 or 128", who, head_dim);
   return H3B_OK;
 }
 
@@ -1677,6 +1693,56 @@ int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_he
   if ((rc = get_ctx(&ctx))) return rc;
   return launch_head_rows(ctx, dtype, 2, a, plan && plan->pairing == H3B_ROPE_HALVES,
                           static_cast<cudaStream_t>(stream));
+}
+
+size_t h3b_attention_prefix_workspace_size(int batch, int n_q, int n_heads, int n_kv_heads,
+                                           int head_dim, int n_prefix, int n_kv) {
+  if (prefix_sizes(batch, n_q, n_heads, n_kv_heads, head_dim, n_prefix, n_kv)) return 0;
+  return prefix_workspace_bytes(head_dim);
+}
+
+int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view* k_prefix,
+                         const h3b_head_view* v_prefix, const h3b_head_view* k,
+                         const h3b_head_view* v, int batch, int n_q, int n_heads,
+                         int n_kv_heads, int head_dim, int n_prefix, int n_kv,
+                         const int32_t* kv_len, const int32_t* q_len, int causal, float scale,
+                         const h3b_head_view* out, void* ws, size_t ws_bytes, void* stream) {
+  const char* me = "attention_prefix";
+  int rc;
+  if (dtype != H3B_DT_BF16 && dtype != H3B_DT_F16)
+    return set_error(H3B_EINVAL, "%s: dtype %d must be bf16 or fp16", me, dtype);
+  if ((rc = prefix_sizes(batch, n_q, n_heads, n_kv_heads, head_dim, n_prefix, n_kv))) return rc;
+  if (!(scale >= 0.f) || !std::isfinite(scale))
+    return set_error(H3B_EINVAL, "%s: scale must be positive and finite (0: 1 / sqrt(head_dim))", me);
+  PrefixArgs a;
+  if ((rc = head_view(me, "q", q, dtype, batch, n_q, n_heads, true, &a.q)) ||
+      (rc = head_view(me, "k_prefix", k_prefix, dtype, 1, n_prefix, n_kv_heads, true, &a.kp)) ||
+      (rc = head_view(me, "v_prefix", v_prefix, dtype, 1, n_prefix, n_kv_heads, true, &a.vp)) ||
+      (rc = head_view(me, "k", k, dtype, batch, n_kv, n_kv_heads, true, &a.k)) ||
+      (rc = head_view(me, "v", v, dtype, batch, n_kv, n_kv_heads, true, &a.v)) ||
+      (rc = head_view(me, "out", out, dtype, batch, n_q, n_heads, true, &a.out)))
+    return rc;
+  if (!al4(kv_len) || !al4(q_len)) return set_error(H3B_EINVAL, "%s: misaligned lengths", me);
+  const size_t need = prefix_workspace_bytes(head_dim);
+  if (!ws || !al16(ws) || ws_bytes < need)
+    return set_error(H3B_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given (16-byte aligned)",
+                     me, need, ws ? ws_bytes : size_t(0));
+  a.batch = batch;
+  a.n_q = n_q;
+  a.heads = n_heads;
+  a.kv_heads = n_kv_heads;
+  a.n_prefix = n_prefix;
+  a.n_kv = n_kv;
+  a.kv_len = kv_len;
+  a.q_len = q_len;
+  a.causal = causal != 0;
+  a.scale_log2 = static_cast<float>(1.4426950408889634 *
+                                    (scale > 0.f ? double(scale) : 1.0 / std::sqrt(double(head_dim))));
+  DevCtx ctx;
+  if ((rc = get_ctx(&ctx))) return rc;
+  if (batch == 0 || n_q == 0) return H3B_OK;
+  return launch_attention_prefix(ctx, dtype == H3B_DT_F16, head_dim, a, ws,
+                                 static_cast<cudaStream_t>(stream));
 }
 
 int h3b_layer_mask(const float* mods_host, int n_blocks, int d, int n_active,

@@ -193,6 +193,29 @@ constexpr size_t head_rows_bwd_bytes(int head_dim) {
 int launch_head_rows(const DevCtx& ctx, int dtype, int mode, HeadRows a, bool halves,
                      cudaStream_t stream);
 
+// Attention over a shared prefix and each sequence's own keys (attention_prefix.cu).
+struct PrefixArgs {
+  HeadView q, kp, vp, k, v, out;
+  int batch = 0, n_q = 0, heads = 0, kv_heads = 0;
+  int n_prefix = 0, n_kv = 0;
+  const int* kv_len = nullptr;  // [batch] or null (n_kv)
+  const int* q_len = nullptr;   // [batch] or null (n_q)
+  int causal = 0;
+  float scale_log2 = 0.f;       // log2(e) * scale
+  // set by the launcher
+  int group = 1;                // heads / kv_heads
+  int prefix_tiles = 0;         // 128-key tiles of the prefix
+  float4* part_o = nullptr;     // [CTA][2 tiles][head_dim / 4][128]
+  float2* part_ml = nullptr;    // [CTA][2 tiles][128]
+  unsigned long long* flags = nullptr;  // [CTA][2 tiles][4 warps]
+  unsigned long long seq = 0;
+  uint32_t* err = nullptr;
+};
+
+size_t prefix_workspace_bytes(int head_dim);
+int launch_attention_prefix(const DevCtx& ctx, bool fp16, int head_dim, PrefixArgs a, void* ws,
+                            cudaStream_t stream);
+
 // ---------------------------------------------------------------- row kernels
 int launch_ln_modulate(const bf16* x, int n, int d, float eps, const float* shift,
                        const float* scale, bf16* h, cudaStream_t stream);

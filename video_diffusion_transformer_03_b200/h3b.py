@@ -142,6 +142,9 @@ _SIGS = {
     "h3b_qk_norm_rope_backward_workspace_size": (_SZ, [_I]),
     "h3b_qk_norm_rope_backward": (_I, [_R, _I, _V, _V, _I, _I, _I, _I, _I, _P, _P, _F, _P, _L, _V,
                                        _V, _V, _V, _P, _P, _P, _SZ, _P]),
+    "h3b_attention_prefix_workspace_size": (_SZ, [_I] * 7),
+    "h3b_attention_prefix": (_I, [_I, _V, _V, _V, _V, _V, _I, _I, _I, _I, _I, _I, _I, _P, _P, _I,
+                                  _F, _V, _P, _SZ, _P]),
 }
 
 EXPORTS = tuple(_SIGS)
@@ -781,6 +784,48 @@ def qk_norm_rope_backward(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: f
         _heads(dq, "dq", shape, dtype, device), kview(dk, "dk"),
         _vector(dq_gain, "dq_gain", hd, device), _vector(dk_gain, "dk_gain", hd, device), wp, wb,
         _raw_stream(stream, device)))
+
+
+def attention_prefix_workspace_size(batch: int, n_q: int, n_heads: int, n_kv_heads: int,
+                                    head_dim: int, n_prefix: int, n_kv: int) -> int:
+    n = int(lib.h3b_attention_prefix_workspace_size(batch, n_q, n_heads, n_kv_heads, head_dim,
+                                                    n_prefix, n_kv))
+    if n == 0:
+        _check(H3B_EINVAL)
+    return n
+
+
+def attention_prefix(q, k_prefix, v_prefix, k, v, out, kv_len=None, q_len=None,
+                     causal: bool = False, scale: float = 0.0, ws=None, stream=None) -> None:
+    """out = attention of q [batch, n_q, heads, head_dim] over the shared k_prefix, v_prefix
+    [n_prefix, kv_heads, head_dim] and the first kv_len[b] (int32 [batch], None: all) of each
+    sequence's own k, v [batch, n_kv, kv_heads, head_dim]; either pair may be None.  causal:
+    the queries are the last q_len[b] tokens of their sequence.  Rows from q_len[b] (None:
+    n_q) on are left as they were.  scale 0: 1 / sqrt(head_dim).  ws: a device buffer of
+    attention_prefix_workspace_size bytes."""
+    shape, dtype, device = _lead(q, "q")
+    if len(shape) != 4:
+        raise TypeError(f"q: expected [batch, n_q, heads, head_dim], got {tuple(shape)}")
+    batch, n_q, heads, hd = shape
+    n_prefix = n_kv = kv_heads = 0
+    vkp = vvp = vk = vv = None
+    if k_prefix is not None:
+        n_prefix, kv_heads = k_prefix.shape[0], k_prefix.shape[-2]
+        ps = (n_prefix, kv_heads, hd)
+        vkp = _heads(k_prefix, "k_prefix", ps, dtype, device)
+        vvp = _heads(v_prefix, "v_prefix", ps, dtype, device)
+    if k is not None:
+        n_kv = k.shape[1]
+        kv_heads = kv_heads or k.shape[-2]
+        ks = (batch, n_kv, kv_heads, hd)
+        vk = _heads(k, "k", ks, dtype, device)
+        vv = _heads(v, "v", ks, dtype, device)
+    wp, wb = _wsargs(ws)
+    _check(lib.h3b_attention_prefix(
+        _DTYPES[dtype], _heads(q, "q", shape, dtype, device), vkp, vvp, vk, vv, batch, n_q, heads,
+        kv_heads, hd, n_prefix, n_kv, _vector(kv_len, "kv_len", batch, device, torch.int32),
+        _vector(q_len, "q_len", batch, device, torch.int32), 1 if causal else 0, scale,
+        _heads(out, "out", shape, dtype, device), wp, wb, _raw_stream(stream, device)))
 
 
 def layer_mask(mods_host: np.ndarray, n_active: int) -> np.ndarray:
