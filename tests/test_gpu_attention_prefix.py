@@ -108,6 +108,8 @@ SIZES = [
     (1, 16, 16, 2, 64, 63, 17), (4, 33, 6, 3, 128, 129, 40), (1, 128, 2, 1, 128, 128, 128),
     (2, 129, 3, 3, 64, 100, 129), (1, 300, 2, 1, 128, 513, 300), (2, 515, 4, 2, 64, 0, 515),
     (1, 1600, 3, 3, 128, 1024, 1600), (70, 2, 3, 3, 64, 20, 9),
+    # keys and values past the L2: their tiles arrive in any order
+    (40, 1, 12, 12, 128, 6000, 1100),
 ]
 
 

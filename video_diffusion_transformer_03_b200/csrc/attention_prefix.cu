@@ -51,28 +51,28 @@ struct WideCfg {
 };
 
 // Total work, and the unit that holds position pos (0 < pos <= total).  All lanes of a warp.
-__device__ inline long long total_work(const PrefixArgs& a, int lane) {
-  long long sum = 0;
+__device__ inline int total_work(const PrefixArgs& a, int lane) {
+  int sum = 0;
   for (int b = lane; b < a.batch; b += 32) sum += a.heads * head_work(a, lens_of(a, b));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
 }
 
-__device__ inline void unit_at(const PrefixArgs& a, long long pos, int lane, Unit& u) {
-  long long base = 0;
+__device__ inline void unit_at(const PrefixArgs& a, int pos, int lane, Unit& u) {
+  int base = 0;
   for (int b0 = 0;; b0 += 32) {
     const int b = b0 + lane;
     Lens l{0, 0};
-    long long w = 0;
+    int w = 0;
     if (b < a.batch) {
       l = lens_of(a, b);
       w = a.heads * head_work(a, l);
     }
-    long long end = w;
+    int end = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, end, o);
+      const int v = __shfl_up_sync(0xffffffffu, end, o);
       if (lane >= o) end += v;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, w > 0 && base + end >= pos);
@@ -81,9 +81,9 @@ __device__ inline void unit_at(const PrefixArgs& a, long long pos, int lane, Uni
       u.b = b0 + src;
       u.len.q = __shfl_sync(0xffffffffu, l.q, src);
       u.len.kv = __shfl_sync(0xffffffffu, l.kv, src);
-      const long long hw = __shfl_sync(0xffffffffu, w, src) / a.heads;
+      const int hw = __shfl_sync(0xffffffffu, w, src) / a.heads;
       base += __shfl_sync(0xffffffffu, end - w, src);
-      u.h = static_cast<int>((pos - base - 1) / hw);
+      u.h = (pos - base - 1) / hw;
       base += u.h * hw;
       break;
     }
@@ -97,8 +97,8 @@ __device__ inline void unit_at(const PrefixArgs& a, long long pos, int lane, Uni
   u.base = base;
   unit_set(a, u);
   const int last = blocks_of(u.len) - 1;
-  while (u.qb < last && u.base + kWorkUnit + static_cast<long long>(u.steps) * u.step_work < pos) {
-    u.base += kWorkUnit + static_cast<long long>(u.steps) * u.step_work;
+  while (u.qb < last && u.base + kWorkUnit + u.steps * u.step_work < pos) {
+    u.base += kWorkUnit + u.steps * u.step_work;
     ++u.qb;
     unit_set(a, u);
   }
@@ -111,7 +111,7 @@ __device__ __forceinline__ float weight_of(float m, float top) {
 
 struct FirstWalk {
   Walk walk;
-  long long total;
+  Cut cut;
 };
 
 template <typename T>
@@ -251,16 +251,16 @@ __global__ void __launch_bounds__(384, 1)
     tmem_relinquish();
   }
   if (warp == 4) {  // this CTA's range
-    const long long total = total_work(a, lane);
+    const Cut all = cut(total_work(a, lane), gridDim.x);
     Walk w{};
-    w.begin = range_begin(total, blockIdx.x, gridDim.x);
-    w.end = range_begin(total, blockIdx.x + 1, gridDim.x);
+    w.begin = all.begin(blockIdx.x);
+    w.end = all.begin(blockIdx.x + 1);
     w.more = w.end > w.begin;
     if (w.more) {
       unit_at(a, w.end, lane, w.u);
       w.settle(a);
     }
-    if (lane == 0) *first = FirstWalk{w, total};
+    if (lane == 0) *first = FirstWalk{w, all};
   }
   tc_fence_before();
   __syncthreads();
@@ -540,13 +540,14 @@ __global__ void __launch_bounds__(384, 1)
       } else {
         // the unit's end: join the states that the CTAs lo .. blockIdx.x - 1 left, in order
         const int me = static_cast<int>(blockIdx.x);
+        const Cut all = first->cut;
         int lo = me;
         float wb = 1.0f;
         if (wk.j0 > 0) {
-          while (lo > 0 && range_begin(first->total, lo, gridDim.x) > wk.u.base) --lo;
+          while (lo > 0 && all.begin(lo) > wk.u.base) --lo;
           float top = m;
           for (int from = lo; from < me && ok; ++from) {
-            if (!has_piece(wk.u, first->total, from, gridDim.x)) continue;
+            if (!has_piece(wk.u, all, from)) continue;
             ok = __all_sync(0xffffffffu, wait_flag(a.flags + (from * 2 + w) * 4 + quarter, a.seq,
                                                    abort_flag, a.err));
             if (ok) top = fmaxf(top, __ldcg(a.part_ml + size_t(from * 2 + w) * 128 + row).x);
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(384, 1)
           wb = weight_of(m, top);
           l *= wb;
           for (int from = lo; from < me; ++from) {
-            if (!has_piece(wk.u, first->total, from, gridDim.x)) continue;
+            if (!has_piece(wk.u, all, from)) continue;
             const float2 ml = __ldcg(a.part_ml + size_t(from * 2 + w) * 128 + row);
             l = fmaf(ml.y, weight_of(ml.x, top), l);
           }
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(384, 1)
             for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(r[q]) * wb;
           }
           for (int from = lo; from < me; ++from) {
-            if (!has_piece(wk.u, first->total, from, gridDim.x)) continue;
+            if (!has_piece(wk.u, all, from)) continue;
             const int src = from * 2 + w;
             const float wa = weight_of(__ldcg(a.part_ml + size_t(src) * 128 + row).x, m);
             const float4* po = a.part_o + size_t(src) * (HD / 4) * 128 + row;
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(384, 1)
         __syncwarp();
         if (lane == 0)
           for (int from = lo; from < me; ++from)
-            if (has_piece(wk.u, first->total, from, gridDim.x)) a.flags[(from * 2 + w) * 4 + quarter] = 0ull;
+            if (has_piece(wk.u, all, from)) a.flags[(from * 2 + w) * 4 + quarter] = 0ull;
       }
       // O may now be overwritten by the next segment's first P V
       tc_fence_before();
@@ -624,16 +625,614 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-// A [batch, tokens, heads, HD] view as a TMA map whose box is 128 tokens by 64 channels.
+// ============================================================================ narrow form
+// Few queries (decoding, a few drafted tokens): what has to be read is the keys and values,
+// each once, and the tensor core's 128 rows are filled with all queries that read the same
+// ones.  A unit of the prefix holds the rows of gt query heads of one key head, of every query,
+// of bt sequences; a unit of a sequence's own keys the same of that sequence alone.  The units'
+// key tiles, laid end to end, are cut into one equal range per CTA, and every part of a unit
+// leaves its rows' state (O, m, l) in the workspace; a second kernel joins the states of each
+// row, of the prefix and of its own, in a fixed order.
+// Within a CTA the steps alternate between two chains, each with its own scores, weights and
+// output accumulator: S, softmax and P V of one step take longer than the step's bytes take to
+// arrive, two such chains do not.  The weights go to tensor memory over the scores they come
+// from (S of the chain's next step is issued behind P V, and the tensor core works in order),
+// which leaves the shared memory to the ring of K and V tiles and to two Q tiles.  A slot of the
+// ring has a full barrier for each chain: the tiles of one slot go to either chain, and a chain
+// that is ahead must not take the barrier's earlier phase, the other chain's, for its own.
+// Roles (384 threads): warp 0 loads; warps 1 and 2 issue chain 0 and 1; warpgroups 1 and 2 are
+// their softmax (warps without rows only keep the barriers' count).
+// TMEM: S0 / P0 [0, 128), S1 / P1 [128, 256), O0 [256, 384), O1 [384, 512).
+
+template <int HD>
+struct NarrowCfg {
+  static constexpr int kNBox = HD / 64;
+  static constexpr uint32_t kTile = kNBox * kBox;
+  static constexpr int kSlots = HD == 128 ? 5 : 11;  // K or V tiles in flight
+  static constexpr size_t kSmem = 1024 + (2 + kSlots) * size_t(kTile) + 1024;
+  static_assert(kSmem <= 232448, "above 227 KB");
+};
+
+struct NarrowMaps {
+  CUtensorMap q_far, q_own, kp, vp, k, v;
+};
+
+// Inclusive sum over the lanes.
+__device__ __forceinline__ int lane_scan(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The CTA's first segment.  All lanes of a warp.
+__device__ inline NarrowWalk narrow_first(const PrefixArgs& a, int lane, int cta) {
+  const int far = narrow_prefix_work(a);
+  // a lane has sequence lane, lane + 32, ...
+  int total = far;
+  Lens l{0, 0};
+  int one = 0, end = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    l = Lens{0, 0};
+    if (b0 + lane < a.batch) l = lens_of(a, b0 + lane);
+    one = narrow_work(narrow_steps(l));
+    end = lane_scan(one * a.own_units, lane);
+    total += __shfl_sync(0xffffffffu, end, 31);
+  }
+  const int ctas = narrow_ctas(total, a.ctas);
+  NarrowWalk w{};
+  if (total == 0 || cta >= ctas) return w;
+  const Cut all = cut(total, ctas);
+  w.begin = all.begin(cta);
+  w.end = all.begin(cta + 1);
+  w.more = w.end > w.begin;
+  if (w.begin < far) {
+    w.u.index = w.begin / narrow_work(a.prefix_tiles);
+    w.u.base = w.u.index * narrow_work(a.prefix_tiles);
+    w.u.b = -1;
+    w.u.steps = a.prefix_tiles;
+  } else {
+    int base = far;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      if (a.batch > 32) {  // else the lanes still hold them
+        l = Lens{0, 0};
+        if (b0 + lane < a.batch) l = lens_of(a, b0 + lane);
+        one = narrow_work(narrow_steps(l));
+        end = lane_scan(one * a.own_units, lane);
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, one > 0 && base + end > w.begin);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        w.u.b = b0 + src;
+        w.u.len.q = __shfl_sync(0xffffffffu, l.q, src);
+        w.u.len.kv = __shfl_sync(0xffffffffu, l.kv, src);
+        w.u.steps = narrow_steps(w.u.len);
+        const int each = narrow_work(w.u.steps);
+        base += __shfl_sync(0xffffffffu, end, src) - each * a.own_units;
+        w.u.in_b = (w.begin - base) / each;
+        w.u.base = base + w.u.in_b * each;
+        w.u.index = a.prefix_units + w.u.b * a.own_units + w.u.in_b;
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, end, 31);
+    }
+  }
+  w.settle(a);
+  return w;
+}
+
+// Key head and first query head of a unit, and the first of its sequences.
+struct NarrowHeads {
+  int kvh, h0, b0, rows;
+};
+__device__ __forceinline__ NarrowHeads narrow_heads(const PrefixArgs& a, const NarrowUnit& u) {
+  NarrowHeads r;
+  int hh;
+  if (u.b < 0) {
+    hh = u.index / a.chunks;
+    const int bc = u.index - hh * a.chunks;
+    r.b0 = bc * a.bt;
+    r.rows = min(a.bt, a.batch - r.b0) * a.gt * a.n_q;
+  } else {
+    hh = u.in_b;
+    r.b0 = u.b;
+    r.rows = a.gt * a.n_q;
+  }
+  r.kvh = hh / a.head_groups;
+  r.h0 = r.kvh * a.group + (hh - r.kvh * a.head_groups) * a.gt;
+  return r;
+}
+
+// Where a segment's state goes: slots of the prefix hold bt * gt * n_q rows, own ones gt * n_q;
+// CTA + unit is different for every segment.
+__device__ __forceinline__ size_t narrow_row(const PrefixArgs& a, bool far, int index, int cta,
+                                             int chain) {
+  const size_t own_rows = size_t(a.gt) * a.n_q, far_rows = own_rows * a.bt;
+  const size_t far_slots = a.prefix_units > 0 ? size_t(a.prefix_units) + a.ctas : 0;
+  if (far) return (size_t(index + cta) * 2 + chain) * far_rows;
+  return far_slots * 2 * far_rows + (size_t(index - a.prefix_units + cta) * 2 + chain) * own_rows;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(384, 1)
+    k_prefix_narrow(const __grid_constant__ NarrowMaps tm, const __grid_constant__ PrefixArgs a) {
+  using Cfg = NarrowCfg<HD>;
+  constexpr bool kF16 = std::is_same_v<T, __half>;
+  constexpr int kSlots = Cfg::kSlots;
+  constexpr uint32_t IDESC_S = kF16 ? idesc_fp16(128, 128, false) : idesc_bf16(128, 128, false);
+  constexpr uint32_t IDESC_PV = kF16 ? idesc_fp16(128, HD, true) : idesc_bf16(128, HD, true);
+  constexpr uint32_t kTmemCols = 512;
+  constexpr uint32_t kOCol = 256;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                  // 2 tiles
+  uint8_t* sKV = sQ + 2 * Cfg::kTile;  // kSlots tiles
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kSlots * Cfg::kTile);
+  uint64_t* q_full = bars + 0;    // [2 tiles]
+  uint64_t* q_empty = bars + 2;   // [2]
+  uint64_t* s_full = bars + 4;    // [2 chains]
+  uint64_t* p_full = bars + 6;    // [2]
+  uint64_t* o_full = bars + 8;    // [2]
+  uint64_t* drain = bars + 10;    // [2]
+  uint64_t* kv_full = bars + 12;  // [2 chains][kSlots]
+  uint64_t* kv_empty = kv_full + 2 * kSlots;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kSlots);
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  NarrowWalk* start = reinterpret_cast<NarrowWalk*>(bars + 48);
+  static_assert(12 + 3 * kSlots + 1 <= 48 && 48 * 8 + sizeof(NarrowWalk) <= 1024, "barrier area");
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 2);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&drain[i], 1);
+    }
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&kv_full[s], 1);
+      mbar_init(&kv_full[kSlots + s], 1);
+      mbar_init(&kv_empty[s], 1);
+    }
+    *abort_flag = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  if (warp == 4) {
+    const NarrowWalk w = narrow_first(a, lane, static_cast<int>(blockIdx.x));
+    if (lane == 0) *start = w;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 4) {
+    regs_dealloc<104>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------------ producer
+      bool ok = true;
+      int slot = 0, n = 0;
+      uint32_t ring_phase = 0;
+      // for the way out: the slots' fills so far, as (chain, parity), and per chain and slot the
+      // parity of the next fill
+      int armed[kSlots];
+#pragma unroll
+      for (int s = 0; s < kSlots; ++s) armed[s] = -1;
+      uint32_t fills[2] = {0, 0};
+      unsigned t = 0;  // steps so far; step t is chain t & 1's
+      int q_armed[2] = {-1, -1};
+      auto load = [&](const CUtensorMap* m, int tok, int kvh, int b) -> bool {
+        if (!wait_bar(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
+          return false;
+        uint64_t* full = &kv_full[(t & 1u) * kSlots + slot];
+        mbar_arrive_expect_tx(full, Cfg::kTile);
+#pragma unroll
+        for (int x = 0; x < Cfg::kNBox; ++x)
+          tma_load_4d(sKV + slot * Cfg::kTile + x * kBox, m, full, 64 * x, tok, kvh, b);
+        uint32_t& f = (t & 1u) ? fills[1] : fills[0];
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (s == slot) armed[s] = static_cast<int>((t & 1u) * 2 + ((f >> s) & 1u));
+        f ^= 1u << slot;
+        if (++slot == kSlots) {
+          slot = 0;
+          ring_phase ^= 1u;
+        }
+        return true;
+      };
+      for (NarrowWalk w = *start; w.more && ok; w.next(a), ++n) {
+        const bool far = w.u.b < 0;
+        const NarrowHeads hd = narrow_heads(a, w.u);
+        const int qb = n & 1;
+        if (n >= 2 && !wait_bar(&q_empty[qb], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag,
+                                a.err, kErrAttnWait)) {
+          ok = false;
+          break;
+        }
+        mbar_arrive_expect_tx(&q_full[qb],
+                              static_cast<uint32_t>((far ? a.bt : 1) * a.gt * a.n_q) * 128u * Cfg::kNBox);
+#pragma unroll
+        for (int x = 0; x < Cfg::kNBox; ++x)
+          tma_load_4d(sQ + qb * Cfg::kTile + x * kBox, far ? &tm.q_far : &tm.q_own, &q_full[qb],
+                      64 * x, 0, hd.h0, hd.b0);
+        q_armed[qb] = (n >> 1) & 1;
+        for (int j = w.j0; j < w.j1 && ok; ++j, ++t)
+          ok = load(far ? &tm.kp : &tm.k, j * 128, hd.kvh, far ? 0 : w.u.b) &&
+               load(far ? &tm.vp : &tm.v, j * 128, hd.kvh, far ? 0 : w.u.b);
+      }
+      if (!ok) {
+        for (int i = 0; i < 2; ++i)
+          if (q_armed[i] >= 0) drain_wait(&q_full[i], static_cast<uint32_t>(q_armed[i]));
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+          if (armed[s] >= 0)
+            drain_wait(&kv_full[(armed[s] >> 1) * kSlots + s], static_cast<uint32_t>(armed[s] & 1));
+      }
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
+      // ------------------------------------------------------------------ MMA issuers
+      const int c = warp - 1;
+      const uint64_t q_desc0 = opaque_u64(sdesc_sw128(smem_u32(sQ), 16, 1024));
+      const uint64_t k_desc0 = opaque_u64(sdesc_sw128(smem_u32(sKV), 16, 1024));
+      const uint64_t v_desc0 = opaque_u64(sdesc_sw128(smem_u32(sKV), kBox, 1024));
+      const uint32_t s_tmem = tmem + c * 128;
+      const uint32_t o_tmem = tmem + kOCol + c * 128;
+      bool ok = true;
+      unsigned t = 0;        // steps of this CTA so far; step t is chain t & 1's
+      uint32_t mine = 0;     // this chain's
+      uint32_t phases = 0;   // parity of this chain's next fill of each slot
+      int n = 0;
+      for (NarrowWalk w = *start; w.more && ok; w.next(a), ++n) {
+        const int qb = n & 1;
+        const int count = w.j1 - w.j0;
+        const unsigned t_end = t + count;
+        bool first = true;
+        if (!wait_bar(&q_full[qb], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, a.err,
+                      kErrAttnWait))
+          break;
+        for (unsigned x = t + ((t ^ c) & 1u); x < t_end; x += 2, ++mine) {
+          const unsigned ik = 2 * x, iv = 2 * x + 1;
+          const int ks = ik % kSlots, vs = iv % kSlots;
+          if (!wait_bar(&kv_full[c * kSlots + ks], (phases >> ks) & 1u, abort_flag, a.err,
+                        kErrAttnWait)) {
+            ok = false;
+            break;
+          }
+          phases ^= 1u << ks;
+          tc_fence_after();
+          const uint64_t q_desc = q_desc0 + static_cast<uint64_t>(qb) * (Cfg::kTile >> 4);
+          const uint64_t k_desc = k_desc0 + static_cast<uint64_t>(ks) * (Cfg::kTile >> 4);
+          if constexpr (HD == 128)
+            umma_f16_x8_kk<kBox / 16>(s_tmem, q_desc, k_desc, IDESC_S, 0u);
+          else
+            umma_f16_x4_kk(s_tmem, q_desc, k_desc, IDESC_S, 0u);
+          tc_commit(&s_full[c]);
+          tc_commit(&kv_empty[ks]);
+          if (x + 2 >= t_end) tc_commit(&q_empty[qb]);
+          if (!wait_bar(&p_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait) ||
+              !wait_bar(&kv_full[c * kSlots + vs], (phases >> vs) & 1u, abort_flag, a.err,
+                        kErrAttnWait)) {
+            ok = false;
+            break;
+          }
+          phases ^= 1u << vs;
+          tc_fence_after();
+          const uint64_t v_desc = v_desc0 + static_cast<uint64_t>(vs) * (Cfg::kTile >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_f16_ts(o_tmem, s_tmem + kk * 8, v_desc + kk * 128, IDESC_PV,
+                        (first && kk == 0) ? 0u : 1u);
+          first = false;
+          tc_commit(&kv_empty[vs]);
+          if (x + 2 >= t_end) tc_commit(&o_full[c]);
+        }
+        if (ok && first) mbar_arrive(&q_empty[qb]);  // a segment of one step, the other chain's
+        t = t_end;
+      }
+      tc_commit(&drain[c]);
+      drain_wait(&drain[c], 0);
+    } else if (warp == 3 && blockIdx.x == 0) {
+      // where every sequence's own work starts, for the joining kernel
+      int base = narrow_prefix_work(a);
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int b = b0 + lane;
+        const int own = b < a.batch ? a.own_units * narrow_work(narrow_steps(lens_of(a, b))) : 0;
+        const int end = lane_scan(own, lane);
+        if (b < a.batch) a.starts[b] = base + end - own;
+        base += __shfl_sync(0xffffffffu, end, 31);
+      }
+      if (lane == 0) a.starts[a.batch] = base;
+    }
+  } else {
+    regs_alloc<200>();
+    // ------------------------------------------------------------------ softmax (chain c)
+    const int c = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_addr = tmem + lane_addr + c * 128;
+    const uint32_t o_addr = tmem + lane_addr + kOCol + c * 128;
+    const float sl2 = a.scale_log2;
+    bool ok = true;
+    unsigned t = 0;
+    uint32_t mine = 0, ends = 0, phases = 0;
+    for (NarrowWalk w = *start; w.more && ok; w.next(a)) {
+      const bool far = w.u.b < 0;
+      const NarrowHeads hd = narrow_heads(a, w.u);
+      const bool warp_on = quarter * 32 < hd.rows;
+      int own_end = w.u.len.kv;
+      if (!far && a.causal) own_end = min(own_end, row % a.n_q + 1 + w.u.len.kv - w.u.len.q);
+      const unsigned t_end = t + (w.j1 - w.j0);
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (unsigned x = t + ((t ^ c) & 1u); x < t_end; x += 2, ++mine) {
+        const int tok = (w.j0 + static_cast<int>(x - t)) * 128;
+        ok = __all_sync(0xffffffffu,
+                        wait_bar(&s_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait));
+        if (!ok) break;
+        if (warp_on) {
+          tc_fence_after();
+          float s[128];
+          {
+            uint32_t r[128];
+            tmem_ld128_sync(s_addr, r);
+#pragma unroll
+            for (int q = 0; q < 128; ++q) s[q] = __uint_as_float(r[q]);
+          }
+          const float alpha = softmax_row(s, (far ? a.n_prefix : own_end) - tok, sl2, m, l);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t r[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              r[q] = pack2<T>(s[half * 64 + 2 * q], s[half * 64 + 2 * q + 1]);
+            tmem_st32(s_addr + half * 32, r);
+          }
+          // O holds the chain's earlier products: S of this step was issued behind them
+          if (!first && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+            for (int cc = 0; cc < HD / 32; ++cc) {
+              uint32_t r[32];
+              tmem_ld32(o_addr + cc * 32, r);
+              tmem_wait_ld(r);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha);
+              tmem_st32(o_addr + cc * 32, r);
+            }
+          }
+          tmem_wait_st();
+        }
+        first = false;
+        const unsigned iv = 2 * x + 1;
+        phases ^= 1u << ((2 * x) % kSlots);
+        if (!far && w.u.len.kv - tok < 128) {
+          // the values behind the sequence's end may be anything (0 * NaN is NaN): zeros
+          const int vs = iv % kSlots;
+          ok = __all_sync(0xffffffffu, wait_bar(&kv_full[c * kSlots + vs], (phases >> vs) & 1u,
+                                                abort_flag, a.err, kErrAttnWait));
+          if (!ok) break;
+          const int from = max(0, w.u.len.kv - tok);
+          uint4* v = reinterpret_cast<uint4*>(sKV + vs * Cfg::kTile);
+          for (int i = row; i < (128 - from) * 8 * Cfg::kNBox; i += 128) {
+            const int b = i / ((128 - from) * 8), e = i - b * (128 - from) * 8;
+            v[b * (kBox / 16) + from * 8 + e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        phases ^= 1u << (iv % kSlots);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[c]);
+      }
+      if (!ok) break;
+      // ---- end of the segment: this chain's state of every row
+      const size_t at = narrow_row(a, far, w.u.index, static_cast<int>(blockIdx.x), c) + row;
+      if (!first) {
+        ok = __all_sync(0xffffffffu,
+                        wait_bar(&o_full[c], ends & 1u, abort_flag, a.err, kErrAttnWait));
+        if (!ok) break;
+        ++ends;
+        if (warp_on) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(o_addr + cc * 32, r);
+            tmem_wait_ld(r);
+            if (row < hd.rows) {
+              float4* d = reinterpret_cast<float4*>(a.part_rows + at * HD + cc * 32);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                d[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                   __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+            }
+          }
+          tc_fence_before();
+        }
+      }
+      if (row < hd.rows) a.part_sums[at] = make_float2(m, l);
+      t = t_end;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// The states of one side (the prefix, the own keys) of a row: CTAs c0 .. c1 hold the unit's
+// steps, two chains each; state i is chain i & 1 of CTA c0 + (i >> 1).
+struct Side {
+  int c0, n;         // n states
+  size_t row, step;  // row of state 0 in the workspace, and from one CTA's to the next
+  size_t chain;      // from chain 0's to chain 1's
+};
+
+__device__ __forceinline__ Side narrow_side(const PrefixArgs& a, const Cut& all, bool far, int index,
+                                            int base, int steps, int in_unit) {
+  Side s;
+  NarrowUnit u;
+  u.base = base;
+  u.steps = steps;
+  // a CTA at either end may hold some of the unit's range but no step of it
+  s.c0 = all.cta_of(base);
+  int c1 = all.cta_of(base + narrow_work(steps) - 1);
+  if (narrow_step_at(u, all.begin(s.c0 + 1)) == 0) ++s.c0;
+  if (narrow_step_at(u, all.begin(c1)) == steps) --c1;
+  s.n = 2 * (c1 - s.c0 + 1);
+  s.row = narrow_row(a, far, index, s.c0, 0) + in_unit;
+  s.chain = size_t(a.gt) * a.n_q * (far ? a.bt : 1);
+  s.step = 2 * s.chain;
+  return s;
+}
+
+// Joins the states of a row: a warp per (sequence, query, head), lanes over the channels.
+// Launched while k_prefix_narrow runs: everything before the wait may overlap it.
+template <typename T, int HD>
+__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixArgs a) {
+  constexpr int kPer = HD / 32;
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int b = row / (a.n_q * a.heads), in_b = row - b * a.n_q * a.heads;
+  const int tok = in_b / a.heads, h = in_b - tok * a.heads;
+  Lens len{0, 0};
+  if (b < a.batch) len = lens_of(a, b);
+  const int kvh = h / a.group, hg = (h - kvh * a.group) / a.gt;
+  const int g = h - kvh * a.group - hg * a.gt;
+  const int hh = kvh * a.head_groups + hg;
+  const int chunk = b / a.bt;
+  const int far_in = ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok, own_in = g * a.n_q + tok;
+  const int own_steps = narrow_steps(len);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (b >= a.batch || tok >= len.q) return;
+  const int total = __ldcg(a.starts + a.batch), start = __ldcg(a.starts + b);
+  Side side[2];
+  side[0].n = side[1].n = 0;
+  if (total > 0) {
+    const Cut all = cut(total, narrow_ctas(total, a.ctas));
+    if (a.prefix_units > 0)
+      side[0] = narrow_side(a, all, true, hh * a.chunks + chunk,
+                            (hh * a.chunks + chunk) * narrow_work(a.prefix_tiles), a.prefix_tiles,
+                            far_in);
+    if (own_steps > 0)
+      side[1] = narrow_side(a, all, false, a.prefix_units + b * a.own_units + hh,
+                            start + hh * narrow_work(own_steps), own_steps, own_in);
+  }
+  // (max, sum) of the first 32 states of each side, a lane each; more are read again
+  auto state = [&](const Side& s, int i) -> float2 {
+    if (i >= s.n) return make_float2(-INFINITY, 0.f);
+    return __ldcg(a.part_sums + s.row + (i >> 1) * s.step + (i & 1) * s.chain);
+  };
+  float2 ml[2];
+  float top = -INFINITY;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    ml[d] = state(side[d], lane);
+    top = fmaxf(top, ml[d].x);
+    for (int i = lane + 32; i < side[d].n; i += 32) top = fmaxf(top, state(side[d], i).x);
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  float l = 0.f, o[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int d = 0; d < 2; ++d) {
+    for (int i0 = 0; i0 < side[d].n; i0 += 32) {
+      const float2 one = i0 == 0 ? ml[d] : state(side[d], i0 + lane);
+      const float wt = weight_of(one.x, top);
+      l = fmaf(one.y, wt, l);
+      const int n = min(32, side[d].n - i0);
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) {
+        const float w = __shfl_sync(0xffffffffu, wt, i);
+        if (w == 0.f) continue;  // a chain without steps, or a state that no longer counts
+        const float* src = a.part_rows +
+                           (side[d].row + ((i0 + i) >> 1) * side[d].step + (i & 1) * side[d].chain) * HD +
+                           lane * kPer;
+        if constexpr (kPer == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+          o[0] = fmaf(v.x, w, o[0]);
+          o[1] = fmaf(v.y, w, o[1]);
+          o[2] = fmaf(v.z, w, o[2]);
+          o[3] = fmaf(v.w, w, o[3]);
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          o[0] = fmaf(v.x, w, o[0]);
+          o[1] = fmaf(v.y, w, o[1]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  const float inv_l = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+  T* dst = static_cast<T*>(a.out.data) + b * a.out.batch + tok * a.out.token + h * a.out.head +
+           lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv_l, o[1] * inv_l),
+                                                pack2<T>(o[2] * inv_l, o[3] * inv_l));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv_l, o[1] * inv_l);
+}
+
+// A [batch, tokens, heads, HD] view as a TMA map whose box is 64 channels of box_tokens tokens
+// of box_heads heads of box_batch sequences.
 bool view_map(CUtensorMap* map, const HeadView& v, bool fp16, int batch, int tokens, int heads,
-              int hd) {
+              int hd, int box_tokens = 128, int box_heads = 1, int box_batch = 1) {
   const cuuint64_t dims[4] = {cuuint64_t(hd), cuuint64_t(tokens), cuuint64_t(heads),
                               cuuint64_t(batch)};
   // (a dimension of size 1 has stride 0 here, which is any valid stride's worth)
   auto bytes = [&](long long st) { return cuuint64_t(st > 0 ? st * 2 : hd * 2); };
   const cuuint64_t strides[3] = {bytes(v.token), bytes(v.head), bytes(v.batch)};
-  const cuuint32_t box[4] = {64, 128, 1, 1};
+  const cuuint32_t box[4] = {64, cuuint32_t(box_tokens), cuuint32_t(box_heads),
+                             cuuint32_t(box_batch)};
   return make_tmap_16bit(map, v.data, fp16, 4, dims, strides, box);
+}
+
+// The maps of the prefix's and of the sequences' keys and values.
+template <typename M>
+bool key_maps(M& tm, const PrefixArgs& a, bool f16, int hd) {
+  bool ok = true;
+  if (a.n_prefix > 0)
+    ok = ok && view_map(&tm.kp, a.kp, f16, 1, a.n_prefix, a.kv_heads, hd) &&
+         view_map(&tm.vp, a.vp, f16, 1, a.n_prefix, a.kv_heads, hd);
+  if (a.n_kv > 0)
+    ok = ok && view_map(&tm.k, a.k, f16, a.batch, a.n_kv, a.kv_heads, hd) &&
+         view_map(&tm.v, a.v, f16, a.batch, a.n_kv, a.kv_heads, hd);
+  // without own keys (or without a prefix) that pair of maps is never used
+  if (a.n_prefix == 0) { tm.kp = tm.k; tm.vp = tm.v; }
+  if (a.n_kv == 0) { tm.k = tm.kp; tm.v = tm.vp; }
+  return ok;
+}
+
+// Dynamic shared memory above 48 KB has to be asked for, once per device.
+template <typename K>
+int allow_smem(const DevCtx& ctx, K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+  const uint64_t bit = 1ull << (ctx.device & 63);
+  if (done.load() & bit) return 0;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes));
+  if (e != cudaSuccess)
+    return set_error(-3, "attention_prefix: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  done.fetch_or(bit);
+  return 0;
 }
 
 template <typename T, int HD>
@@ -641,27 +1240,11 @@ int launch_wide(const DevCtx& ctx, PrefixArgs a, cudaStream_t stream) {
   using Cfg = WideCfg<HD>;
   constexpr bool f16 = std::is_same_v<T, __half>;
   Maps tm;
-  bool ok = view_map(&tm.q, a.q, f16, a.batch, a.n_q, a.heads, HD);
-  if (a.n_prefix > 0)
-    ok = ok && view_map(&tm.kp, a.kp, f16, 1, a.n_prefix, a.kv_heads, HD) &&
-         view_map(&tm.vp, a.vp, f16, 1, a.n_prefix, a.kv_heads, HD);
-  if (a.n_kv > 0)
-    ok = ok && view_map(&tm.k, a.k, f16, a.batch, a.n_kv, a.kv_heads, HD) &&
-         view_map(&tm.v, a.v, f16, a.batch, a.n_kv, a.kv_heads, HD);
-  if (!ok) return set_error(-3, "attention_prefix: cuTensorMapEncodeTiled failed");
-  // without own keys (or without a prefix) that pair of maps is never used
-  if (a.n_prefix == 0) { tm.kp = tm.k; tm.vp = tm.v; }
-  if (a.n_kv == 0) { tm.k = tm.kp; tm.v = tm.vp; }
+  if (!view_map(&tm.q, a.q, f16, a.batch, a.n_q, a.heads, HD) || !key_maps(tm, a, f16, HD))
+    return set_error(-3, "attention_prefix: cuTensorMapEncodeTiled failed");
   auto kernel = k_prefix_wide<T, HD>;
-  static std::atomic<uint64_t> attr_done{0};
-  const uint64_t bit = 1ull << (ctx.device & 63);
-  if (!(attr_done.load() & bit)) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Cfg::kSmem));
-    if (e != cudaSuccess)
-      return set_error(-3, "attention_prefix: cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    attr_done.fetch_or(bit);
-  }
+  static std::atomic<uint64_t> done{0};
+  if (int rc = allow_smem(ctx, kernel, Cfg::kSmem, done)) return rc;
   const long long units = 1ll * a.batch * a.heads * ((a.n_q + kBlockQ - 1) / kBlockQ);
   const int grid = static_cast<int>(
       std::min<long long>(units * kMaxPieces, std::min(ctx.num_sms, kMaxSkCtas)));
@@ -670,26 +1253,109 @@ int launch_wide(const DevCtx& ctx, PrefixArgs a, cudaStream_t stream) {
   return check_launch("attention_prefix");
 }
 
+template <typename T, int HD>
+int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
+  using Cfg = NarrowCfg<HD>;
+  constexpr bool f16 = std::is_same_v<T, __half>;
+  NarrowMaps tm;
+  if (!view_map(&tm.q_own, a.q, f16, a.batch, a.n_q, a.heads, HD, a.n_q, a.gt, 1) ||
+      !view_map(&tm.q_far, a.q, f16, a.batch, a.n_q, a.heads, HD, a.n_q, a.gt, a.bt) ||
+      !key_maps(tm, a, f16, HD))
+    return set_error(-3, "attention_prefix: cuTensorMapEncodeTiled failed");
+  auto kernel = k_prefix_narrow<T, HD>;
+  static std::atomic<uint64_t> done{0};
+  if (int rc = allow_smem(ctx, kernel, Cfg::kSmem, done)) return rc;
+  kernel<<<a.ctas, 384, Cfg::kSmem, stream>>>(tm, a);
+  if (int rc = check_launch("attention_prefix")) return rc;
+  // launched while the first kernel runs; it waits for it before it reads
+  const long long rows = 1ll * a.batch * a.n_q * a.heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD>, a);
+  return check_launch("attention_prefix join");
+}
+
+template <typename T, int HD>
+int launch_form(const DevCtx& ctx, const PrefixArgs& a, bool narrow, cudaStream_t stream) {
+  return narrow ? launch_narrow<T, HD>(ctx, a, stream) : launch_wide<T, HD>(ctx, a, stream);
+}
+
+// The narrow form's units.
+void narrow_units(PrefixArgs& a) {
+  a.gt = std::min(a.group, 128 / a.n_q);
+  a.head_groups = (a.group + a.gt - 1) / a.gt;
+  a.gt = (a.group + a.head_groups - 1) / a.head_groups;
+  a.bt = a.n_prefix > 0 ? std::min(a.batch, 128 / (a.gt * a.n_q)) : 1;
+  a.chunks = (a.batch + a.bt - 1) / a.bt;
+  a.bt = (a.batch + a.chunks - 1) / a.chunks;
+  a.own_units = a.kv_heads * a.head_groups;
+  a.prefix_units = a.n_prefix > 0 ? a.own_units * a.chunks : 0;
+}
+
+// Rows of the narrow form's workspace.
+size_t narrow_rows(const PrefixArgs& a) {
+  const size_t own = size_t(a.gt) * a.n_q;
+  size_t rows = 2 * (size_t(a.batch) * a.own_units + kMaxSkCtas) * own;
+  if (a.prefix_units > 0) rows += 2 * (size_t(a.prefix_units) + kMaxSkCtas) * own * a.bt;
+  return rows;
+}
+
+// The narrow form, for at most this many queries a sequence.
+constexpr int kNarrowQueries = 64;
+
+bool use_narrow(PrefixArgs a) {
+  if (a.n_q > kNarrowQueries || 1ll * a.batch * a.heads > (1 << 20)) return false;
+  narrow_units(a);
+  return narrow_work_cap(a) * 2 <= kMaxWork;
+}
+
 }  // namespace
 
-size_t prefix_workspace_bytes(int head_dim) {
+size_t prefix_workspace_bytes(PrefixArgs a, int head_dim) {
+  a.group = a.heads / a.kv_heads;
+  if (a.batch == 0 || a.n_q == 0) return 16;
+  if (use_narrow(a)) {
+    narrow_units(a);
+    return narrow_rows(a) * (head_dim * 4 + 8) + (size_t(a.batch) + 1) * 4;
+  }
   return size_t(kMaxSkCtas) * 2 * 128 * (head_dim * 4 + 8) + size_t(kMaxSkCtas) * 2 * 4 * 8;
 }
 
 int launch_attention_prefix(const DevCtx& ctx, bool fp16, int head_dim, PrefixArgs a, void* ws,
                             cudaStream_t stream) {
-  uint8_t* p = static_cast<uint8_t*>(ws);
-  a.part_o = reinterpret_cast<float4*>(p);
-  p += size_t(kMaxSkCtas) * 2 * 128 * head_dim * 4;
-  a.part_ml = reinterpret_cast<float2*>(p);
-  p += size_t(kMaxSkCtas) * 2 * 128 * 8;
-  a.flags = reinterpret_cast<unsigned long long*>(p);
   a.err = ctx.err_flag;
   a.prefix_tiles = (a.n_prefix + 127) / 128;
   a.group = a.heads / a.kv_heads;
+  a.ctas = std::min(ctx.num_sms, kMaxSkCtas);
+  const bool narrow = use_narrow(a);
+  if (!narrow && wide_work_cap(a) * 2 > kMaxWork)
+    return set_error(-1, "attention_prefix: too much work for one call");
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  if (narrow) {
+    narrow_units(a);
+    const size_t rows = narrow_rows(a);
+    a.part_rows = reinterpret_cast<float*>(p);
+    a.part_sums = reinterpret_cast<float2*>(p + rows * head_dim * 4);
+    a.starts = reinterpret_cast<int*>(p + rows * (head_dim * 4 + 8));
+  } else {
+    a.part_o = reinterpret_cast<float4*>(p);
+    p += size_t(kMaxSkCtas) * 2 * 128 * head_dim * 4;
+    a.part_ml = reinterpret_cast<float2*>(p);
+    p += size_t(kMaxSkCtas) * 2 * 128 * 8;
+    a.flags = reinterpret_cast<unsigned long long*>(p);
+  }
   if (head_dim == 128)
-    return fp16 ? launch_wide<__half, 128>(ctx, a, stream) : launch_wide<bf16, 128>(ctx, a, stream);
-  return fp16 ? launch_wide<__half, 64>(ctx, a, stream) : launch_wide<bf16, 64>(ctx, a, stream);
+    return fp16 ? launch_form<__half, 128>(ctx, a, narrow, stream)
+                : launch_form<bf16, 128>(ctx, a, narrow, stream);
+  return fp16 ? launch_form<__half, 64>(ctx, a, narrow, stream)
+              : launch_form<bf16, 64>(ctx, a, narrow, stream);
 }
 
 }  // namespace h3b

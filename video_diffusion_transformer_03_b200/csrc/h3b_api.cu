@@ -1698,7 +1698,14 @@ int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_he
 size_t h3b_attention_prefix_workspace_size(int batch, int n_q, int n_heads, int n_kv_heads,
                                            int head_dim, int n_prefix, int n_kv) {
   if (prefix_sizes(batch, n_q, n_heads, n_kv_heads, head_dim, n_prefix, n_kv)) return 0;
-  return prefix_workspace_bytes(head_dim);
+  PrefixArgs a;
+  a.batch = batch;
+  a.n_q = n_q;
+  a.heads = n_heads;
+  a.kv_heads = n_kv_heads;
+  a.n_prefix = n_prefix;
+  a.n_kv = n_kv;
+  return prefix_workspace_bytes(a, head_dim);
 }
 
 int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view* k_prefix,
@@ -1723,7 +1730,8 @@ int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view*
       (rc = head_view(me, "out", out, dtype, batch, n_q, n_heads, true, &a.out)))
     return rc;
   if (!al4(kv_len) || !al4(q_len)) return set_error(H3B_EINVAL, "%s: misaligned lengths", me);
-  const size_t need = prefix_workspace_bytes(head_dim);
+  const size_t need = h3b_attention_prefix_workspace_size(batch, n_q, n_heads, n_kv_heads, head_dim,
+                                                          n_prefix, n_kv);
   if (!ws || !al16(ws) || ws_bytes < need)
     return set_error(H3B_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given (16-byte aligned)",
                      me, need, ws ? ws_bytes : size_t(0));

@@ -205,6 +205,13 @@ struct PrefixArgs {
   // set by the launcher
   int group = 1;                // heads / kv_heads
   int prefix_tiles = 0;         // 128-key tiles of the prefix
+  // narrow form: query heads and sequences of a unit, and the units' counts
+  int gt = 1, head_groups = 1, bt = 1, chunks = 1;
+  int prefix_units = 0, own_units = 0;
+  int ctas = 0;
+  float* part_rows = nullptr;   // [slot][rows][head_dim] O, prefix slots then own ones
+  float2* part_sums = nullptr;  // [slot][rows] (running max, row sum)
+  int* starts = nullptr;        // [batch + 1] where a sequence's own work starts; the total
   float4* part_o = nullptr;     // [CTA][2 tiles][head_dim / 4][128]
   float2* part_ml = nullptr;    // [CTA][2 tiles][128]
   unsigned long long* flags = nullptr;  // [CTA][2 tiles][4 warps]
@@ -212,7 +219,8 @@ struct PrefixArgs {
   uint32_t* err = nullptr;
 };
 
-size_t prefix_workspace_bytes(int head_dim);
+// Sizes of a (batch, n_q, heads, kv_heads, n_prefix, n_kv) are all it reads.
+size_t prefix_workspace_bytes(PrefixArgs a, int head_dim);
 int launch_attention_prefix(const DevCtx& ctx, bool fp16, int head_dim, PrefixArgs a, void* ws,
                             cudaStream_t stream);
 

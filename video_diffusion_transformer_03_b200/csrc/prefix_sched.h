@@ -1,5 +1,6 @@
-// The wide attention's schedule: how the work of a batch is cut into one range per CTA, and
-// the walk over a range.  Host and device, so that it can be enumerated without a GPU.
+// The schedules of the shared-prefix attention: how the work of a batch is cut into one range
+// per CTA, and the walk over a range, of its wide and of its narrow form.  Host and device, so
+// that they can be enumerated without a GPU.
 #pragma once
 
 #include "kernels.h"
@@ -7,6 +8,8 @@
 namespace h3b {
 
 constexpr int kBlockQ = 256;
+// Work is counted in 32 bits: calls of more than this are refused (at 2^31, some 10^8 tiles).
+constexpr long long kMaxWork = (1ll << 31) - 1;
 
 __host__ __device__ inline int clamp_len(int v, int top) { return v < 0 ? 0 : v > top ? top : v; }
 
@@ -27,7 +30,7 @@ struct Unit {
   Lens len;
   int steps;        // key tiles (at least one, so that rows without keys are written)
   int step_work;    // cost of a step
-  long long base;
+  int base;
 };
 
 // Cost of a step with two query tiles and of one whose second tile is empty, and of a unit's
@@ -49,29 +52,30 @@ __host__ __device__ inline void unit_cost(const PrefixArgs& a, const Lens& l, in
 }
 
 // Work of one head of a sequence.
-__host__ __device__ inline long long head_work(const PrefixArgs& a, const Lens& l) {
+__host__ __device__ inline int head_work(const PrefixArgs& a, const Lens& l) {
   const int nb = blocks_of(l);
   if (nb == 0) return 0;
-  long long sum = 0;
+  int sum = 0;
   int steps, w;
   if (a.causal) {
     for (int qb = 0; qb < nb; ++qb) {
       unit_cost(a, l, qb, steps, w);
-      sum += kWorkUnit + static_cast<long long>(steps) * w;
+      sum += kWorkUnit + steps * w;
     }
     return sum;
   }
   unit_cost(a, l, nb - 1, steps, w);
-  sum = kWorkUnit + static_cast<long long>(steps) * w;
-  return sum + (nb - 1ll) * (kWorkUnit + static_cast<long long>(steps) * kWorkTwo);
+  sum = kWorkUnit + steps * w;
+  return sum + (nb - 1) * (kWorkUnit + steps * kWorkTwo);
 }
 
 // The first step of the unit at or after position pos (steps where there is none).
-__host__ __device__ inline int step_at(const Unit& u, long long pos) {
-  const long long r = pos - u.base - kWorkUnit;
+__host__ __device__ inline int step_at(const Unit& u, int pos) {
+  const int r = pos - u.base - kWorkUnit;
   if (r <= 0) return 0;
-  const long long j = (r + u.step_work - 1) / u.step_work;
-  return j < u.steps ? static_cast<int>(j) : u.steps;
+  // (constant divisors: a shift and a multiplication)
+  const int j = u.step_work == kWorkTwo ? (r + kWorkTwo - 1) / kWorkTwo : (r + kWorkOne - 1) / kWorkOne;
+  return j < u.steps ? j : u.steps;
 }
 
 __host__ __device__ inline void unit_set(const PrefixArgs& a, Unit& u) {
@@ -96,24 +100,35 @@ __host__ __device__ inline bool unit_prev(const PrefixArgs& a, Unit& u) {
     u.qb = blocks_of(u.len) - 1;
   }
   unit_set(a, u);
-  u.base -= kWorkUnit + static_cast<long long>(u.steps) * u.step_work;
+  u.base -= kWorkUnit + u.steps * u.step_work;
   return true;
 }
 
-__host__ __device__ inline long long range_begin(long long total, int cta, int ctas) {
-  return total * cta / ctas;
-}
+// The cut of `total` into equal ranges: the first `more` of them are `each` + 1 long, the
+// others `each`.
+struct Cut {
+  int each, more;
+  __host__ __device__ inline int begin(int cta) const {
+    return each * cta + (cta < more ? cta : more);
+  }
+  // the range that holds position pos
+  __host__ __device__ inline int cta_of(int pos) const {
+    const int head = more * (each + 1);
+    return pos < head ? pos / (each + 1) : more + (pos - head) / each;
+  }
+};
+__host__ __device__ inline Cut cut(int total, int ctas) { return Cut{total / ctas, total % ctas}; }
 
 // Whether CTA `cta` holds steps of the unit.
-__host__ __device__ inline bool has_piece(const Unit& u, long long total, int cta, int ctas) {
-  return step_at(u, range_begin(total, cta, ctas)) < step_at(u, range_begin(total, cta + 1, ctas));
+__host__ __device__ inline bool has_piece(const Unit& u, const Cut& c, int cta) {
+  return step_at(u, c.begin(cta)) < step_at(u, c.begin(cta + 1));
 }
 
 // A CTA's range [begin, end) of positions, walked from its end; one segment is the part of a
 // unit that lies in it, steps [j0, j1).
 struct Walk {
   Unit u;
-  long long begin, end;
+  int begin, end;
   int j0, j1;
   bool more;
 
@@ -133,5 +148,103 @@ struct Walk {
     settle(a);
   }
 };
+
+// The most work a call of these sizes can have.
+inline long long wide_work_cap(const PrefixArgs& a) {
+  const long long tiles = (a.n_prefix + 127) / 128 + (a.n_kv + 127) / 128;
+  return 1ll * a.batch * a.heads * ((a.n_q + kBlockQ - 1) / kBlockQ) * (kWorkUnit + (tiles + 1) * kWorkTwo);
+}
+
+// ------------------------------------------------------------------------- narrow form
+// Units: the prefix's first, (key head, group of gt query heads, chunk of bt sequences), then
+// every sequence's own, (sequence, key head, group of query heads).  A unit's rows are its
+// sequences' queries of those heads; its steps the 128-key tiles of the prefix or of the
+// sequence.  Units without keys or queries have no work.
+constexpr int kNarrowStep = 4, kNarrowUnit = 4;  // cost of a step; of a unit's start and end
+
+struct NarrowUnit {
+  int index;        // prefix units, then batch x own units
+  int b;            // sequence; -1: of the prefix
+  int in_b;         // own: index inside the sequence
+  Lens len;
+  int steps;
+  int base;
+};
+
+__host__ __device__ inline int narrow_work(int steps) {
+  return steps > 0 ? kNarrowUnit + steps * kNarrowStep : 0;
+}
+__host__ __device__ inline int narrow_steps(const Lens& l) {
+  return l.q > 0 ? (l.kv + 127) / 128 : 0;
+}
+__host__ __device__ inline int narrow_prefix_work(const PrefixArgs& a) {
+  return a.prefix_units * narrow_work(a.prefix_tiles);
+}
+
+__host__ __device__ inline int narrow_step_at(const NarrowUnit& u, int pos) {
+  const int r = pos - u.base - kNarrowUnit;
+  if (r <= 0) return 0;
+  const int j = (r + kNarrowStep - 1) / kNarrowStep;
+  return j < u.steps ? j : u.steps;
+}
+
+// The first of a sequence's units at or after sequence b that has work.
+__host__ __device__ inline bool narrow_own(const PrefixArgs& a, NarrowUnit& u, int b) {
+  for (; b < a.batch; ++b) {
+    u.len = lens_of(a, b);
+    u.steps = narrow_steps(u.len);
+    if (u.steps == 0) continue;
+    u.b = b;
+    u.in_b = 0;
+    u.index = a.prefix_units + b * a.own_units;
+    return true;
+  }
+  return false;
+}
+
+__host__ __device__ inline bool narrow_next(const PrefixArgs& a, NarrowUnit& u) {
+  u.base += narrow_work(u.steps);
+  if (u.b < 0) {
+    if (++u.index < a.prefix_units) return true;
+    return narrow_own(a, u, 0);
+  }
+  if (++u.in_b < a.own_units) {
+    ++u.index;
+    return true;
+  }
+  return narrow_own(a, u, u.b + 1);
+}
+
+// CTAs that get a range: as many as there are, but at least min_work for each.
+__host__ __device__ inline int narrow_ctas(int total, int most) {
+  const int n = total / (2 * kNarrowStep + kNarrowUnit);
+  return n < 1 ? 1 : n < most ? n : most;
+}
+
+struct NarrowWalk {
+  NarrowUnit u;
+  int begin, end;
+  int j0, j1;
+  bool more;
+
+  __host__ __device__ inline void settle(const PrefixArgs& a) {
+    while (more) {
+      j0 = narrow_step_at(u, begin);
+      j1 = narrow_step_at(u, end);
+      if (j0 < j1) return;
+      more = u.base + narrow_work(u.steps) < end && narrow_next(a, u);
+    }
+  }
+  __host__ __device__ inline void next(const PrefixArgs& a) {
+    more = u.base + narrow_work(u.steps) < end && narrow_next(a, u);
+    settle(a);
+  }
+};
+
+inline long long narrow_work_cap(const PrefixArgs& a) {
+  const long long far = (a.n_prefix + 127) / 128, own = (a.n_kv + 127) / 128;
+  return a.prefix_units * (kNarrowUnit + far * kNarrowStep) +
+         1ll * a.batch * a.own_units * (kNarrowUnit + own * kNarrowStep);
+}
 
 }  // namespace h3b
