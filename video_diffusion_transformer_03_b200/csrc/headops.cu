@@ -71,43 +71,83 @@ __device__ __forceinline__ void store_raw(T* p, int c0, int c1, const Raw<T>& r)
   }
 }
 
+// The four pairs of a lane, members a and b apart, as packed fp32: a[0] holds pairs 0 and 1.
+// Packed arithmetic does two of them in one issue slot, which is what these kernels run out of
+// first once enough loads are in flight.
+struct Pairs {
+  uint64_t a[2], b[2];
+};
+
 template <typename T>
-__device__ __forceinline__ void widen(const Raw<T>& r, float (&f)[8]) {
-  if constexpr (std::is_same_v<T, float>) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(r.w[i]);
-  } else if constexpr (std::is_same_v<T, __half>) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r.w[i]));
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 v = unpack_bf16x2(r.w[i]);
-      f[2 * i] = v.x;
-      f[2 * i + 1] = v.y;
-    }
-  }
+__device__ __forceinline__ float2 two(uint32_t u) {
+  if constexpr (std::is_same_v<T, __half>) return __half22float2(*reinterpret_cast<const __half2*>(&u));
+  else return unpack_bf16x2(u);
 }
 
 template <typename T>
-__device__ __forceinline__ void narrow(const float (&f)[8], Raw<T>& r) {
-  if constexpr (std::is_same_v<T, float>) {
+__device__ __forceinline__ uint32_t two(float x, float y) {
+  if constexpr (std::is_same_v<T, __half>) return pack_f16x2(x, y);
+  else return pack_bf16x2(x, y);
+}
+
+template <typename T, bool HALVES>
+__device__ __forceinline__ Pairs widen(const Raw<T>& r) {
+  Pairs p;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(f[i]);
-  } else if constexpr (std::is_same_v<T, __half>) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-      r.w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  for (int i = 0; i < 2; ++i) {
+    if constexpr (std::is_same_v<T, float>) {
+      const float f0 = __uint_as_float(r.w[HALVES ? 2 * i : 4 * i]);
+      const float f1 = __uint_as_float(r.w[HALVES ? 2 * i + 1 : 4 * i + 1]);
+      const float f2 = __uint_as_float(r.w[HALVES ? 4 + 2 * i : 4 * i + 2]);
+      const float f3 = __uint_as_float(r.w[HALVES ? 5 + 2 * i : 4 * i + 3]);
+      p.a[i] = HALVES ? pack_f32x2(f0, f1) : pack_f32x2(f0, f2);
+      p.b[i] = HALVES ? pack_f32x2(f2, f3) : pack_f32x2(f1, f3);
+    } else {
+      const float2 u = two<T>(r.w[HALVES ? i : 2 * i]), v = two<T>(r.w[HALVES ? 2 + i : 2 * i + 1]);
+      p.a[i] = HALVES ? pack_f32x2(u.x, u.y) : pack_f32x2(u.x, v.x);
+      p.b[i] = HALVES ? pack_f32x2(v.x, v.y) : pack_f32x2(u.y, v.y);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
   }
+  return p;
+}
+
+template <typename T, bool HALVES>
+__device__ __forceinline__ Raw<T> narrow(const Pairs& p) {
+  Raw<T> r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    float a0, a1, b0, b1;
+    unpack_f32x2(p.a[i], a0, a1);
+    unpack_f32x2(p.b[i], b0, b1);
+    if constexpr (std::is_same_v<T, float>) {
+      r.w[HALVES ? 2 * i : 4 * i] = __float_as_uint(a0);
+      r.w[HALVES ? 2 * i + 1 : 4 * i + 2] = __float_as_uint(a1);
+      r.w[HALVES ? 4 + 2 * i : 4 * i + 1] = __float_as_uint(b0);
+      r.w[HALVES ? 5 + 2 * i : 4 * i + 3] = __float_as_uint(b1);
+    } else {
+      r.w[HALVES ? i : 2 * i] = HALVES ? two<T>(a0, a1) : two<T>(a0, b0);
+      r.w[HALVES ? 2 + i : 2 * i + 1] = HALVES ? two<T>(b0, b1) : two<T>(a1, b1);
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ Pairs mul(const Pairs& p, uint64_t f) {
+  Pairs r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    r.a[i] = mul_f32x2(p.a[i], f);
+    r.b[i] = mul_f32x2(p.b[i], f);
+  }
+  return r;
+}
+// sum of the products of the eight channels
+__device__ __forceinline__ float dot8(const Pairs& p, const Pairs& q) {
+  const uint64_t x = fma_f32x2(p.a[0], q.a[0], mul_f32x2(p.b[0], q.b[0]));
+  const uint64_t y = fma_f32x2(p.a[1], q.a[1], mul_f32x2(p.b[1], q.b[1]));
+  float lo, hi;
+  unpack_f32x2(add_f32x2(x, y), lo, hi);
+  return lo + hi;
 }
 
 // sin and cos of 2 pi t.  Adding 1.5 * 2^52 rounds t to the nearest integer.
@@ -117,16 +157,19 @@ __device__ __forceinline__ void sincos_turns(double t, float& s, float& c) {
   sincospif(2.0f * static_cast<float>(t - n), &s, &c);
 }
 
-// The pairs of f turned by (c, s).
-template <bool HALVES>
-__device__ __forceinline__ void rotate(float (&f)[8], const float (&c)[4], const float (&s)[4]) {
+// A turn, with a factor on each member before it (the gains): a -> a ac - b bs, b -> a as + b bc.
+struct Turn {
+  uint64_t ac[2], nbs[2], as[2], bc[2];  // nbs = -bs
+};
+
+__device__ __forceinline__ Pairs rotate(const Pairs& p, const Turn& t) {
+  Pairs r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int ia = HALVES ? i : 2 * i, ib = HALVES ? 4 + i : 2 * i + 1;
-    const float a = f[ia], b = f[ib];
-    f[ia] = fmaf(a, c[i], -(b * s[i]));
-    f[ib] = fmaf(a, s[i], b * c[i]);
+  for (int i = 0; i < 2; ++i) {
+    r.a[i] = fma_f32x2(p.a[i], t.ac[i], mul_f32x2(p.b[i], t.nbs[i]));
+    r.b[i] = fma_f32x2(p.a[i], t.as[i], mul_f32x2(p.b[i], t.bc[i]));
   }
+  return r;
 }
 
 // Sum over the LPH lanes of a head.
@@ -135,6 +178,16 @@ __device__ __forceinline__ float head_sum(float v) {
 #pragma unroll
   for (int o = LPH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Channel of pair i's members behind the first of a lane's eight contiguous ones.
+template <bool HALVES>
+__device__ __forceinline__ constexpr int member_a(int i) {
+  return HALVES ? i : 2 * i;
+}
+template <bool HALVES>
+__device__ __forceinline__ constexpr int member_b(int i) {
+  return HALVES ? 4 + i : 2 * i + 1;
 }
 
 // A group is kPass passes of 32 / LPH heads.  An item is one token, or (parts > 1, where
@@ -172,15 +225,19 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
   const int groups = (heads + kGroup - 1) / kGroup;
   const unsigned n_items = static_cast<unsigned>(a.rows) * parts;
 
-  double turns[4] = {0.0, 0.0, 0.0, 0.0};
+  // this lane computes kOwn of its slot's four angles; lanes of the other heads the others
+  constexpr int kOwn = 4 / kHeads > 0 ? 4 / kHeads : 1;
+  double turns[kOwn];
   uint32_t axes = 0;
-  float gain[8];
-  float acc[8];
+  Pairs gain, acc;
   bool have_lane = false;
   const float inv_hd = 1.0f / static_cast<float>(a.head_dim);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+  for (int i = 0; i < kOwn; ++i) turns[i] = 0.0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) acc.a[i] = acc.b[i] = 0ull;
 
+  const long long in_step = kHeads * in.head, out_step = kHeads * out.head;
   for (unsigned item = block * kWarps + (threadIdx.x >> 5); item < n_items;
        item += blocks * kWarps) {
     unsigned row = item, b = 0;
@@ -196,53 +253,93 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
       b = row / static_cast<unsigned>(a.tokens);
       t = row - b * static_cast<unsigned>(a.tokens);
     }
-    const T* src = static_cast<const T*>(in.data) + b * in.batch + t * in.token;
+    // pointers to this lane's channels of the group's first head, stepped head by head
+    const int first = g0 * kGroup + sub;
+    const T* src = static_cast<const T*>(in.data) + b * in.batch + t * in.token + first * in.head;
+    T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token + first * out.head;
     const T* grd = nullptr;
-    if constexpr (kBwd)
-      grd = static_cast<const T*>(a.grad[w].data) + b * a.grad[w].batch + t * a.grad[w].token;
-    T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token;
+    long long grd_step = 0;
+    if constexpr (kBwd) {
+      grd = static_cast<const T*>(a.grad[w].data) + b * a.grad[w].batch + t * a.grad[w].token +
+            first * a.grad[w].head;
+      grd_step = kHeads * a.grad[w].head;
+    }
+    int left = heads - first;  // heads from this lane's on
 
     Raw<T> x[kPass], gy[kPass];
-    auto load = [&](int g) {
+    auto load = [&](int n) {
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        const int h = g * kGroup + i * kHeads + sub;
-        const bool on = live && h < heads;
+        const bool on = live && i * kHeads < n;
         x[i] = Raw<T>{};
-        if (on) load_raw<T, HALVES>(src + h * in.head, c0, c1, x[i]);
+        if (on) load_raw<T, HALVES>(src, c0, c1, x[i]);
+        src += in_step;
         if constexpr (kBwd) {
           gy[i] = Raw<T>{};
-          if (on) load_raw<T, HALVES>(grd + h * a.grad[w].head, c0, c1, gy[i]);
+          if (on) load_raw<T, HALVES>(grd, c0, c1, gy[i]);
+          grd += grd_step;
         }
       }
     };
-    load(g0);
+    load(left);
     if (!have_lane) {
       // this lane's constants, behind its first loads
       have_lane = true;
       if (turned) {
-        const double2 t0 = *reinterpret_cast<const double2*>(a.turns + slot * 4);
-        const double2 t1 = *reinterpret_cast<const double2*>(a.turns + slot * 4 + 2);
-        turns[0] = t0.x; turns[1] = t0.y; turns[2] = t1.x; turns[3] = t1.y;
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) turns[i] = a.turns[slot * 4 + (sub * kOwn + i) % 4];
         axes = *reinterpret_cast<const uint32_t*>(a.axis + slot * 4);
       }
       if constexpr (MODE != kModeRope) {
         const float* g = w ? a.k_gain : a.q_gain;
+        float ga[4], gb[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          gain[i] = (g != nullptr && live) ? __ldg(g + (i < 4 ? c0 + i : c1 + i - 4)) : 1.f;
+        for (int i = 0; i < 4; ++i) {
+          const bool on = g != nullptr && live;
+          ga[i] = on ? __ldg(g + (HALVES && turned ? c0 + i : slot * 8 + member_a<HALVES>(i))) : 1.f;
+          gb[i] = on ? __ldg(g + (HALVES && turned ? c1 + i : slot * 8 + member_b<HALVES>(i))) : 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          gain.a[i] = pack_f32x2(ga[2 * i], ga[2 * i + 1]);
+          gain.b[i] = pack_f32x2(gb[2 * i], gb[2 * i + 1]);
+        }
       }
     }
-    float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
-    if (turned) {
-      // pairs past the rotated width have turns 0: they stay
-      const float* pos = a.pos + b * a.pos_batch + static_cast<size_t>(t) * a.n_axes;
+    Turn turn;
+    {
+      float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+      if (a.n_pairs > 0) {
+        const float* pos = a.pos + b * a.pos_batch + static_cast<size_t>(t) * a.n_axes;
+        float oc[kOwn], os[kOwn];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (slot * 4 + i < a.n_pairs)
-          sincos_turns(static_cast<double>(__ldg(pos + ((axes >> (8 * i)) & 0xffu))) * turns[i],
-                       sn[i], cs[i]);
-        if (kBwd || (MODE == kModeRope && a.inverse)) sn[i] = -sn[i];
+        for (int i = 0; i < kOwn; ++i) {
+          // (a pair past the rotated width has turns 0: it stays)
+          const int p = (sub * kOwn + i) % 4;
+          sincos_turns(static_cast<double>(__ldg(pos + ((axes >> (8 * p)) & 0xffu))) * turns[i], os[i],
+                       oc[i]);
+          if (kBwd || (MODE == kModeRope && a.inverse)) os[i] = -os[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kOwn == 4) {
+            cs[i] = oc[i];
+            sn[i] = os[i];
+          } else {
+            cs[i] = __shfl_sync(0xffffffffu, oc[i % kOwn], slot + (i / kOwn) * LPH);
+            sn[i] = __shfl_sync(0xffffffffu, os[i % kOwn], slot + (i / kOwn) * LPH);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t c = pack_f32x2(cs[2 * i], cs[2 * i + 1]), s = pack_f32x2(sn[2 * i], sn[2 * i + 1]);
+        const uint64_t n = pack_f32x2(-sn[2 * i], -sn[2 * i + 1]);
+        const bool folded = MODE == kModeNorm;  // y = rstd R(g x): the gains go into the turn
+        turn.ac[i] = folded ? mul_f32x2(gain.a[i], c) : c;
+        turn.nbs[i] = folded ? mul_f32x2(gain.b[i], n) : n;
+        turn.as[i] = folded ? mul_f32x2(gain.a[i], s) : s;
+        turn.bc[i] = folded ? mul_f32x2(gain.b[i], c) : c;
       }
     }
     for (int g = g0; g < g1; ++g) {
@@ -252,56 +349,64 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
         xc[i] = x[i];
         if constexpr (kBwd) gc[i] = gy[i];
       }
-      if (g + 1 < g1) load(g + 1);
+      if (g + 1 < g1) load(left - kGroup);
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        const int h = g * kGroup + i * kHeads + sub;
-        float f[8];
-        widen<T>(xc[i], f);
+        Pairs f = widen<T, HALVES>(xc[i]);
         if constexpr (MODE != kModeRope) {
-          float ss = 0.f;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) ss = fmaf(f[c], f[c], ss);
-          const float rstd = rsqrtf(head_sum<LPH>(ss) * inv_hd + a.eps);
+          const float rstd = rsqrtf(head_sum<LPH>(dot8(f, f)) * inv_hd + a.eps);
+          const uint64_t r2 = pack_f32x2(rstd, rstd);
           if constexpr (!kBwd) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] *= rstd * gain[c];
+            f = mul(f, r2);
           } else {
-            float z[8];
-            widen<T>(gc[i], z);
-            rotate<HALVES>(z, cs, sn);
-            float dot = 0.f;
+            Pairs z = rotate(widen<T, HALVES>(gc[i]), turn);
+            f = mul(f, r2);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              f[c] *= rstd;
-              acc[c] = fmaf(z[c], f[c], acc[c]);
-              z[c] *= gain[c];
-              dot = fmaf(z[c], f[c], dot);
+            for (int k = 0; k < 2; ++k) {
+              acc.a[k] = fma_f32x2(z.a[k], f.a[k], acc.a[k]);
+              acc.b[k] = fma_f32x2(z.b[k], f.b[k], acc.b[k]);
+              z.a[k] = mul_f32x2(z.a[k], gain.a[k]);
+              z.b[k] = mul_f32x2(z.b[k], gain.b[k]);
             }
-            dot = head_sum<LPH>(dot) * inv_hd;
+            const float dot = -head_sum<LPH>(dot8(z, f)) * inv_hd;
+            const uint64_t d2 = pack_f32x2(dot, dot);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) f[c] = rstd * fmaf(-f[c], dot, z[c]);
+            for (int k = 0; k < 2; ++k) {
+              f.a[k] = fma_f32x2(f.a[k], d2, z.a[k]);
+              f.b[k] = fma_f32x2(f.b[k], d2, z.b[k]);
+            }
+            f = mul(f, r2);
           }
         }
-        if constexpr (!kBwd) rotate<HALVES>(f, cs, sn);
-        if (live && h < heads) {
-          Raw<T> y;
-          narrow<T>(f, y);
-          store_raw<T, HALVES>(dst + h * out.head, c0, c1, y);
-        }
+        if constexpr (!kBwd) f = rotate(f, turn);
+        if (live && i * kHeads < left) store_raw<T, HALVES>(dst, c0, c1, narrow<T, HALVES>(f));
+        dst += out_step;
       }
+      left -= kGroup;
     }
   }
   if constexpr (kBwd) {
     // the block's share of the gain's gradient: lanes of the same slot, then its warps in
     // order, then one row [head_dim] of the workspace
     __shared__ float red[kWarps][LPH * 8];
+    float va[4], vb[4];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float v = acc[c];
+    for (int i = 0; i < 2; ++i) {
+      unpack_f32x2(acc.a[i], va[2 * i], va[2 * i + 1]);
+      unpack_f32x2(acc.b[i], vb[2 * i], vb[2 * i + 1]);
+    }
 #pragma unroll
-      for (int o = LPH; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (sub == 0 && live) red[threadIdx.x >> 5][c < 4 ? c0 + c : c1 + c - 4] = v;
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int o = LPH; o < 32; o <<= 1) {
+        va[i] += __shfl_xor_sync(0xffffffffu, va[i], o);
+        vb[i] += __shfl_xor_sync(0xffffffffu, vb[i], o);
+      }
+      if (sub == 0 && live) {
+        float* r = red[threadIdx.x >> 5];
+        r[HALVES && turned ? c0 + i : slot * 8 + member_a<HALVES>(i)] = va[i];
+        r[HALVES && turned ? c1 + i : slot * 8 + member_b<HALVES>(i)] = vb[i];
+      }
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.head_dim; c += kWarps * 32) {
