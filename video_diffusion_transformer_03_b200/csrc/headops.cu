@@ -197,7 +197,11 @@ constexpr int pass_count() {
   return (MODE == kModeNormBwd || sizeof(T) == 4) ? 1 : 2;
 }
 
-// Blocks that are on an SM at a time (their registers: 64, 80 and 128 a thread); the grid is
+// What an item costs beside its groups of heads (its angles, and its first loads' latency), in
+// groups.
+constexpr int kItemCost = 1;
+
+// Blocks that are on an SM at a time (their registers: 64, 80 and 96 a thread); the grid is
 // that many a SM at most.
 constexpr int blocks_per_sm(int mode) {
   return mode == kModeNormBwd ? kHeadRowsBwdPerSm : mode == kModeNorm ? 6 : 8;
@@ -450,19 +454,18 @@ int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
   const long long most = 1ll * blocks_per_sm(MODE) * sms;
   // Tokens alone keep an SM busy from about 24 of its warps on; with fewer, a token's groups
   // of heads are dealt to several warps, each of which computes the token's angles again.
-  long long items[2], total = 0;
+  long long items[2], cost[2];
   for (int w = 0; w < 2; ++w) {
     const int groups = (a.heads[w] + kGroup - 1) / kGroup;
     const long long want = a.rows > 0 ? (24ll * sms + a.rows - 1) / a.rows : 1;
     a.parts[w] = static_cast<int>(std::max<long long>(1, std::min<long long>(groups, want)));
     items[w] = groups > 0 ? a.rows * a.parts[w] : 0;
-    total += items[w] * groups / a.parts[w];
+    cost[w] = items[w] * (kItemCost + groups / a.parts[w]);
   }
   // q's share of the blocks is its share of the work
   long long blocks[2];
   for (int w = 0; w < 2; ++w) {
-    const int groups = (a.heads[w] + kGroup - 1) / kGroup;
-    const long long share = total > 0 ? (most * items[w] * groups / a.parts[w]) / total : 0;
+    const long long share = items[w] > 0 ? most * cost[w] / (cost[0] + cost[1]) : 0;
     blocks[w] = std::min<long long>((items[w] + kWarps - 1) / kWarps, std::max<long long>(share, 1));
   }
   a.q_blocks = static_cast<int>(blocks[0]);

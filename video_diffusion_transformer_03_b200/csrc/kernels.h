@@ -183,7 +183,7 @@ struct HeadRows {
 };
 
 // Blocks of the backward pass on an SM; each writes a row of the workspace.
-constexpr int kHeadRowsBwdPerSm = 4;
+constexpr int kHeadRowsBwdPerSm = 5;
 constexpr size_t head_rows_bwd_bytes(int head_dim) {
   // one block more than the cap: q and k get at least one each
   return (size_t(kHeadRowsBwdPerSm) * kMaxSkCtas + 1) * head_dim * sizeof(float);
