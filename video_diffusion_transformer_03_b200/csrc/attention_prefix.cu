@@ -133,6 +133,17 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// wait_bar, without its look at the timer before the first polls: most waits here end within
+// a microsecond, and the timer's read alone takes a good part of that.
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t* err,
+                                          uint32_t code) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_bar(bar, parity, abort_flag, err, code);
+}
+
 __device__ __forceinline__ bool wait_flag(const unsigned long long* f, unsigned long long seq,
                                           volatile uint32_t* abort_flag, uint32_t* err) {
   if (ld_acquire_u64(f) == seq) return true;
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(384, 1)
       int armed[kRing] = {-1, -1, -1};
       int q_armed = -1;
       auto load = [&](bool is_v, const Unit& u, int j) -> bool {
-        if (!wait_bar(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
+        if (!wait_soon(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
           return false;
         mbar_arrive_expect_tx(&kv_full[slot], Cfg::kTile);
         const bool far = j < a.prefix_tiles;
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(384, 1)
         if (pj >= 0) ok = load(true, pu, pj);
         for (int j = w.j0; j < w.j1 && ok; ++j) {
           if (j == w.j0) {
-            if (n > 0 && !wait_bar(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, a.err,
+            if (n > 0 && !wait_soon(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, a.err,
                                    kErrAttnWait)) {
               ok = false;
               break;
@@ -346,7 +357,7 @@ __global__ void __launch_bounds__(384, 1)
       const uint32_t s_tmem = tmem + w * 128;
       const uint32_t o_tmem = tmem + kOCol + w * 128;
       auto ring_take = [&](int& s_out) -> bool {
-        if (!wait_bar(&kv_full[slot], ring_phase, abort_flag, a.err, kErrAttnWait)) return false;
+        if (!wait_soon(&kv_full[slot], ring_phase, abort_flag, a.err, kErrAttnWait)) return false;
         s_out = slot;
         if (++slot == kRing) {
           slot = 0;
@@ -356,12 +367,12 @@ __global__ void __launch_bounds__(384, 1)
       };
       auto issue_s = [&](bool here, bool first, bool last) -> bool {
         if (first &&
-            !wait_bar(q_full, static_cast<uint32_t>(n) & 1u, abort_flag, a.err, kErrAttnWait))
+            !wait_soon(q_full, static_cast<uint32_t>(n) & 1u, abort_flag, a.err, kErrAttnWait))
           return false;
         int ksl;
         if (!ring_take(ksl)) return false;
         if (here) {
-          if (cnt >= 1 && !wait_bar(&s_free[w], static_cast<uint32_t>(cnt - 1) & 1u, abort_flag,
+          if (cnt >= 1 && !wait_soon(&s_free[w], static_cast<uint32_t>(cnt - 1) & 1u, abort_flag,
                                     a.err, kErrAttnWait))
             return false;
           tc_fence_after();
@@ -383,10 +394,10 @@ __global__ void __launch_bounds__(384, 1)
         if (here) {
           // the tile's previous segment must have read O out before it is overwritten
           if (first && units > 0 &&
-              !wait_bar(&o_empty[w], static_cast<uint32_t>(units - 1) & 1u, abort_flag, a.err,
+              !wait_soon(&o_empty[w], static_cast<uint32_t>(units - 1) & 1u, abort_flag, a.err,
                         kErrAttnWait))
             return false;
-          if (!wait_bar(&p_full[w], static_cast<uint32_t>(pvc) & 1u, abort_flag, a.err,
+          if (!wait_soon(&p_full[w], static_cast<uint32_t>(pvc) & 1u, abort_flag, a.err,
                         kErrAttnWait))
             return false;
           tc_fence_after();
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(384, 1)
       if (a.causal) own_end = min(own_end, q0 + row + 1 + wk.u.len.kv - wk.u.len.q);
       float m = -INFINITY, l = 0.f;
       for (int j = wk.j0; j < wk.j1; ++j, ++c, ++t) {
-        ok = __all_sync(0xffffffffu, wait_bar(&s_full[w], static_cast<uint32_t>(c) & 1u, abort_flag,
+        ok = __all_sync(0xffffffffu, wait_soon(&s_full[w], static_cast<uint32_t>(c) & 1u, abort_flag,
                                               a.err, kErrAttnWait));
         if (!ok) break;
         tc_fence_after();
@@ -463,7 +474,7 @@ __global__ void __launch_bounds__(384, 1)
         const float alpha = softmax_row(s, lim, sl2, m, l);
         if (c >= 1) {
           // the P tile is free, and O complete, once the tile's previous P V has finished
-          ok = __all_sync(0xffffffffu, wait_bar(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
+          ok = __all_sync(0xffffffffu, wait_soon(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
                                                 abort_flag, a.err, kErrAttnWait));
           if (!ok) break;
         }
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(384, 1)
           const int idx = 2 * t + (j + 1 == wk.j1 ? 1 : 2);
           const int vsl = idx % kRing;
           ok = __all_sync(0xffffffffu,
-                          wait_bar(&kv_full[vsl], static_cast<uint32_t>(idx / kRing) & 1u,
+                          wait_soon(&kv_full[vsl], static_cast<uint32_t>(idx / kRing) & 1u,
                                    abort_flag, a.err, kErrAttnWait));
           if (!ok) break;
           const int from = max(0, wk.u.len.kv - tok);
@@ -514,7 +525,7 @@ __global__ void __launch_bounds__(384, 1)
       }
       if (!ok) break;
       // ---- end of the segment: O holds every P V product once the last one completes
-      ok = __all_sync(0xffffffffu, wait_bar(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
+      ok = __all_sync(0xffffffffu, wait_soon(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
                                             abort_flag, a.err, kErrAttnWait));
       if (!ok) break;
       tc_fence_after();
@@ -835,7 +846,7 @@ __global__ void __launch_bounds__(384, 1)
       unsigned t = 0;  // steps so far; step t is chain t & 1's
       int q_armed[2] = {-1, -1};
       auto load = [&](const CUtensorMap* m, int tok, int kvh, int b) -> bool {
-        if (!wait_bar(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
+        if (!wait_soon(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
           return false;
         uint64_t* full = &kv_full[(t & 1u) * kSlots + slot];
         mbar_arrive_expect_tx(full, Cfg::kTile);
@@ -857,7 +868,7 @@ __global__ void __launch_bounds__(384, 1)
         const bool far = w.u.b < 0;
         const NarrowHeads hd = narrow_heads(a, w.u);
         const int qb = n & 1;
-        if (n >= 2 && !wait_bar(&q_empty[qb], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag,
+        if (n >= 2 && !wait_soon(&q_empty[qb], static_cast<uint32_t>((n >> 1) - 1) & 1u, abort_flag,
                                 a.err, kErrAttnWait)) {
           ok = false;
           break;
@@ -899,13 +910,13 @@ __global__ void __launch_bounds__(384, 1)
         const int count = w.j1 - w.j0;
         const unsigned t_end = t + count;
         bool first = true;
-        if (!wait_bar(&q_full[qb], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, a.err,
+        if (!wait_soon(&q_full[qb], static_cast<uint32_t>(n >> 1) & 1u, abort_flag, a.err,
                       kErrAttnWait))
           break;
         for (unsigned x = t + ((t ^ c) & 1u); x < t_end; x += 2, ++mine) {
           const unsigned ik = 2 * x, iv = 2 * x + 1;
           const int ks = ik % kSlots, vs = iv % kSlots;
-          if (!wait_bar(&kv_full[c * kSlots + ks], (phases >> ks) & 1u, abort_flag, a.err,
+          if (!wait_soon(&kv_full[c * kSlots + ks], (phases >> ks) & 1u, abort_flag, a.err,
                         kErrAttnWait)) {
             ok = false;
             break;
@@ -921,8 +932,8 @@ __global__ void __launch_bounds__(384, 1)
           tc_commit(&s_full[c]);
           tc_commit(&kv_empty[ks]);
           if (x + 2 >= t_end) tc_commit(&q_empty[qb]);
-          if (!wait_bar(&p_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait) ||
-              !wait_bar(&kv_full[c * kSlots + vs], (phases >> vs) & 1u, abort_flag, a.err,
+          if (!wait_soon(&p_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait) ||
+              !wait_soon(&kv_full[c * kSlots + vs], (phases >> vs) & 1u, abort_flag, a.err,
                         kErrAttnWait)) {
             ok = false;
             break;
@@ -943,17 +954,6 @@ __global__ void __launch_bounds__(384, 1)
       }
       tc_commit(&drain[c]);
       drain_wait(&drain[c], 0);
-    } else if (warp == 3 && blockIdx.x == 0) {
-      // where every sequence's own work starts, for the joining kernel
-      int base = narrow_prefix_work(a);
-      for (int b0 = 0; b0 < a.batch; b0 += 32) {
-        const int b = b0 + lane;
-        const int own = b < a.batch ? a.own_units * narrow_work(narrow_steps(lens_of(a, b))) : 0;
-        const int end = lane_scan(own, lane);
-        if (b < a.batch) a.starts[b] = base + end - own;
-        base += __shfl_sync(0xffffffffu, end, 31);
-      }
-      if (lane == 0) a.starts[a.batch] = base;
     }
   } else {
     regs_alloc<200>();
@@ -980,7 +980,7 @@ __global__ void __launch_bounds__(384, 1)
       for (unsigned x = t + ((t ^ c) & 1u); x < t_end; x += 2, ++mine) {
         const int tok = (w.j0 + static_cast<int>(x - t)) * 128;
         ok = __all_sync(0xffffffffu,
-                        wait_bar(&s_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait));
+                        wait_soon(&s_full[c], mine & 1u, abort_flag, a.err, kErrAttnWait));
         if (!ok) break;
         if (warp_on) {
           tc_fence_after();
@@ -1020,7 +1020,7 @@ __global__ void __launch_bounds__(384, 1)
         if (!far && w.u.len.kv - tok < 128) {
           // the values behind the sequence's end may be anything (0 * NaN is NaN): zeros
           const int vs = iv % kSlots;
-          ok = __all_sync(0xffffffffu, wait_bar(&kv_full[c * kSlots + vs], (phases >> vs) & 1u,
+          ok = __all_sync(0xffffffffu, wait_soon(&kv_full[c * kSlots + vs], (phases >> vs) & 1u,
                                                 abort_flag, a.err, kErrAttnWait));
           if (!ok) break;
           const int from = max(0, w.u.len.kv - tok);
@@ -1041,7 +1041,7 @@ __global__ void __launch_bounds__(384, 1)
       const size_t at = narrow_row(a, far, w.u.index, static_cast<int>(blockIdx.x), c) + row;
       if (!first) {
         ok = __all_sync(0xffffffffu,
-                        wait_bar(&o_full[c], ends & 1u, abort_flag, a.err, kErrAttnWait));
+                        wait_soon(&o_full[c], ends & 1u, abort_flag, a.err, kErrAttnWait));
         if (!ok) break;
         ++ends;
         if (warp_on) {
@@ -1102,51 +1102,68 @@ __device__ __forceinline__ Side narrow_side(const PrefixArgs& a, const Cut& all,
   return s;
 }
 
-// Joins the states of a row: a warp per (sequence, query, head), lanes over the channels.
-// Launched while k_prefix_narrow runs: everything before the wait may overlap it.
-template <typename T, int HD>
+// Joins the states of a row of the output: WARPS warps per (sequence, query, head), each with
+// its share of the states, lanes over the channels.  Launched while k_prefix_narrow runs: the
+// schedule is worked out before the wait for it, only the states' two loads come after.
+template <typename T, int HD, int WARPS>
 __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixArgs a) {
   constexpr int kPer = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  constexpr int kRows = 4 / WARPS;  // rows of a block
+  __shared__ int s_start[kRows], s_total;
+  __shared__ float s_part[WARPS > 1 ? 4 : 1][HD + 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int in_block = warp / WARPS, sub = warp % WARPS;
+  const int row = blockIdx.x * kRows + in_block;
   const int b = row / (a.n_q * a.heads), in_b = row - b * a.n_q * a.heads;
   const int tok = in_b / a.heads, h = in_b - tok * a.heads;
+  if (warp == 0) {
+    // where the rows' sequences' own work starts
+    int base = narrow_prefix_work(a);
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int own =
+          b0 + lane < a.batch ? a.own_units * narrow_work(narrow_steps(lens_of(a, b0 + lane))) : 0;
+      const int end = lane_scan(own, lane);
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if ((blockIdx.x * kRows + r) / (a.n_q * a.heads) == b0 + lane) s_start[r] = base + end - own;
+      base += __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) s_total = base;
+  }
+  __syncthreads();
+  const int total = s_total;
   Lens len{0, 0};
   if (b < a.batch) len = lens_of(a, b);
-  const int kvh = h / a.group, hg = (h - kvh * a.group) / a.gt;
-  const int g = h - kvh * a.group - hg * a.gt;
-  const int hh = kvh * a.head_groups + hg;
-  const int chunk = b / a.bt;
-  const int far_in = ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok, own_in = g * a.n_q + tok;
-  const int own_steps = narrow_steps(len);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (b >= a.batch || tok >= len.q) return;
-  const int total = __ldcg(a.starts + a.batch), start = __ldcg(a.starts + b);
+  const bool on = b < a.batch && tok < len.q;
   Side side[2];
   side[0].n = side[1].n = 0;
-  if (total > 0) {
+  if (on && total > 0) {
     const Cut all = cut(total, narrow_ctas(total, a.ctas));
-    if (a.prefix_units > 0)
-      side[0] = narrow_side(a, all, true, hh * a.chunks + chunk,
-                            (hh * a.chunks + chunk) * narrow_work(a.prefix_tiles), a.prefix_tiles,
-                            far_in);
-    if (own_steps > 0)
+    const int kvh = h / a.group, hg = (h - kvh * a.group) / a.gt;
+    const int g = h - kvh * a.group - hg * a.gt, hh = kvh * a.head_groups + hg;
+    if (a.prefix_units > 0) {
+      const int chunk = b / a.bt, index = hh * a.chunks + chunk;
+      side[0] = narrow_side(a, all, true, index, index * narrow_work(a.prefix_tiles), a.prefix_tiles,
+                            ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok);
+    }
+    const int steps = narrow_steps(len);
+    if (steps > 0)
       side[1] = narrow_side(a, all, false, a.prefix_units + b * a.own_units + hh,
-                            start + hh * narrow_work(own_steps), own_steps, own_in);
+                            s_start[in_block] + hh * narrow_work(steps), steps, g * a.n_q + tok);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // (max, sum) of the first 32 states of each side, a lane each; more are read again
   auto state = [&](const Side& s, int i) -> float2 {
     if (i >= s.n) return make_float2(-INFINITY, 0.f);
     return __ldcg(a.part_sums + s.row + (i >> 1) * s.step + (i & 1) * s.chain);
   };
   float2 ml[2];
-  float top = -INFINITY;
 #pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    ml[d] = state(side[d], lane);
-    top = fmaxf(top, ml[d].x);
+  for (int d = 0; d < 2; ++d) ml[d] = state(side[d], lane);
+  float top = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+  for (int d = 0; d < 2; ++d)
     for (int i = lane + 32; i < side[d].n; i += 32) top = fmaxf(top, state(side[d], i).x);
-  }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
   float l = 0.f, o[kPer];
@@ -1160,7 +1177,7 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
       l = fmaf(one.y, wt, l);
       const int n = min(32, side[d].n - i0);
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
+      for (int i = sub; i < n; i += WARPS) {
         const float w = __shfl_sync(0xffffffffu, wt, i);
         if (w == 0.f) continue;  // a chain without steps, or a state that no longer counts
         const float* src = a.part_rows +
@@ -1182,6 +1199,18 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+  if constexpr (WARPS > 1) {
+    // the warps' shares, added in order
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) s_part[warp][lane * kPer + e] = o[e];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int v = 1; v < WARPS; ++v)
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] += s_part[warp + v][lane * kPer + e];
+  }
+  if (!on) return;
   const float inv_l = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
   T* dst = static_cast<T*>(a.out.data) + b * a.out.batch + tok * a.out.token + h * a.out.head +
            lane * kPer;
@@ -1267,10 +1296,13 @@ int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
   if (int rc = allow_smem(ctx, kernel, Cfg::kSmem, done)) return rc;
   kernel<<<a.ctas, 384, Cfg::kSmem, stream>>>(tm, a);
   if (int rc = check_launch("attention_prefix")) return rc;
-  // launched while the first kernel runs; it waits for it before it reads
+  // launched while the first kernel runs; it waits for it before it reads.  A unit of the prefix
+  // is spread over about ctas / prefix_units CTAs, two states each: from eight states on four
+  // warps share a row.
   const long long rows = 1ll * a.batch * a.n_q * a.heads;
+  const bool many = a.prefix_units > 0 && 2 * a.ctas >= 8 * a.prefix_units;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (rows + 3) / 4));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -1278,7 +1310,8 @@ int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD>, a);
+  if (many) cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 4>, a);
+  else cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 1>, a);
   return check_launch("attention_prefix join");
 }
 
@@ -1323,7 +1356,7 @@ size_t prefix_workspace_bytes(PrefixArgs a, int head_dim) {
   if (a.batch == 0 || a.n_q == 0) return 16;
   if (use_narrow(a)) {
     narrow_units(a);
-    return narrow_rows(a) * (head_dim * 4 + 8) + (size_t(a.batch) + 1) * 4;
+    return narrow_rows(a) * (head_dim * 4 + 8);
   }
   return size_t(kMaxSkCtas) * 2 * 128 * (head_dim * 4 + 8) + size_t(kMaxSkCtas) * 2 * 4 * 8;
 }
@@ -1343,7 +1376,6 @@ int launch_attention_prefix(const DevCtx& ctx, bool fp16, int head_dim, PrefixAr
     const size_t rows = narrow_rows(a);
     a.part_rows = reinterpret_cast<float*>(p);
     a.part_sums = reinterpret_cast<float2*>(p + rows * head_dim * 4);
-    a.starts = reinterpret_cast<int*>(p + rows * (head_dim * 4 + 8));
   } else {
     a.part_o = reinterpret_cast<float4*>(p);
     p += size_t(kMaxSkCtas) * 2 * 128 * head_dim * 4;

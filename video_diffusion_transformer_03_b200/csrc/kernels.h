@@ -211,7 +211,6 @@ struct PrefixArgs {
   int ctas = 0;
   float* part_rows = nullptr;   // [slot][rows][head_dim] O, prefix slots then own ones
   float2* part_sums = nullptr;  // [slot][rows] (running max, row sum)
-  int* starts = nullptr;        // [batch + 1] where a sequence's own work starts; the total
   float4* part_o = nullptr;     // [CTA][2 tiles][head_dim / 4][128]
   float2* part_ml = nullptr;    // [CTA][2 tiles][128]
   unsigned long long* flags = nullptr;  // [CTA][2 tiles][4 warps]
