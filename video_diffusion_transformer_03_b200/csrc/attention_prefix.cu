@@ -37,14 +37,16 @@ namespace h3b {
 namespace {
 
 constexpr uint32_t kBox = 128 * 128;  // 128 rows of 128 bytes, swizzled
+constexpr int kRing = 3;
 constexpr int kMaxPieces = 8;  // CTAs that share a unit, on average, at most
 
 template <int HD>
 struct WideCfg {
   static constexpr int kNBox = HD / 64;
-  static constexpr uint32_t kTile = kNBox * kBox;    // 128 rows of Q, K or V
-  static constexpr int kRing = HD == 128 ? 4 : 8;    // K or V tiles
-  static constexpr size_t kSmem = 1024 + (2 + kRing) * size_t(kTile) + 2 * size_t(kBox) + 512;
+  static constexpr uint32_t kTile = kNBox * kBox;  // 128 rows of Q, K or V
+  static constexpr uint32_t kPBytes = 2 * kBox;
+  static constexpr size_t kSmem = 1024 + 2 * size_t(kTile) + 2 * size_t(kPBytes) +
+                                  size_t(kRing) * kTile + 512;
   static_assert(kSmem <= 232448, "above 227 KB");
 };
 
@@ -166,13 +168,12 @@ __device__ __forceinline__ bool wait_flag(const unsigned long long* f, unsigned 
   return true;
 }
 
-// Softmax of N of a row's scores, those from lim on hidden, against the running maximum m
+// Softmax of a row's 128 scores s, those from lim on hidden, against the running maximum m
 // (base 2).  First the maximum: the factor by which O has to be multiplied (1 where m stays).
-template <int N>
-__device__ __forceinline__ float softmax_max(float (&s)[N], int lim, float sl2, float& m) {
-  if (lim < N) {
+__device__ __forceinline__ float softmax_max(float (&s)[128], int lim, float sl2, float& m) {
+  if (lim < 128) {
 #pragma unroll
-    for (int q = 0; q < N; ++q)
+    for (int q = 0; q < 128; ++q)
       if (q >= lim) s[q] = -INFINITY;
   }
   float m8[8];
@@ -180,7 +181,7 @@ __device__ __forceinline__ float softmax_max(float (&s)[N], int lim, float sl2, 
   for (int i = 0; i < 8; ++i) {
     m8[i] = fmaxf(s[i], s[8 + i]);
 #pragma unroll
-    for (int q = 16; q < N; q += 16) m8[i] = max3(m8[i], s[q + i], s[q + 8 + i]);
+    for (int q = 16; q < 128; q += 16) m8[i] = max3(m8[i], s[q + i], s[q + 8 + i]);
   }
   const float mxs =
       max3(max3(m8[0], m8[1], m8[2]), max3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7])) * sl2;
@@ -193,14 +194,14 @@ __device__ __forceinline__ float softmax_max(float (&s)[N], int lim, float sl2, 
 }
 
 // Then the weights: s becomes P, packed; l the new running sum.
-template <typename T, int N>
-__device__ __forceinline__ void softmax_exp(const float (&s)[N], float sl2, float m, float alpha,
-                                            float& l, uint32_t (&p)[N / 2]) {
+template <typename T>
+__device__ __forceinline__ void softmax_exp(const float (&s)[128], float sl2, float m, float alpha,
+                                            float& l, uint32_t (&p)[64]) {
   const float base = m == -INFINITY ? 0.0f : -m;
   const uint64_t sl2x2 = pack_f32x2(sl2, sl2), base2 = pack_f32x2(base, base);
   uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-  for (int q = 0; q < N; q += 2) {
+  for (int q = 0; q < 128; q += 2) {
     float x0, x1;
     const uint64_t x2 = fma_f32x2(pack_f32x2(s[q], s[q + 1]), sl2x2, base2);
     unpack_f32x2(x2, x0, x1);
@@ -222,9 +223,8 @@ template <typename T, int HD>
 __global__ void __launch_bounds__(384, 1)
     k_prefix_wide(const __grid_constant__ Maps tm, const __grid_constant__ PrefixArgs a) {
   using Cfg = WideCfg<HD>;
-  constexpr int kRing = Cfg::kRing;
   constexpr bool kF16 = std::is_same_v<T, __half>;
-  constexpr uint32_t IDESC_S = kF16 ? idesc_fp16(128, 64, false) : idesc_bf16(128, 64, false);
+  constexpr uint32_t IDESC_S = kF16 ? idesc_fp16(128, 128, false) : idesc_bf16(128, 128, false);
   constexpr uint32_t IDESC_PV = kF16 ? idesc_fp16(128, HD, true) : idesc_bf16(128, HD, true);
   constexpr uint32_t kTmemCols = 512;
   constexpr uint32_t kOCol = 256;
@@ -232,23 +232,24 @@ __global__ void __launch_bounds__(384, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                        // 2 tiles
-  uint8_t* sKV = sQ + 2 * Cfg::kTile;        // kRing slots
-  uint8_t* sOut = sKV + kRing * Cfg::kTile;  // 2 tiles x 128 rows x 64 channels
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sOut + 2 * kBox);
+  uint8_t* sQ = smem;                      // 2 tiles
+  uint8_t* sP = sQ + 2 * Cfg::kTile;       // 2 tiles
+  uint8_t* sKV = sP + 2 * Cfg::kPBytes;    // kRing slots
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sKV + kRing * Cfg::kTile);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
-  uint64_t* s_full = bars + 2;    // [2 tiles][2 halves]
-  uint64_t* p_full = bars + 6;    // [2][2]
-  uint64_t* pv_done = bars + 10;  // [2]
-  uint64_t* o_full = bars + 12;   // [2]
-  uint64_t* drain = bars + 14;    // [2 issuers]
-  uint64_t* kv_full = bars + 16;  // [kRing]
-  uint64_t* kv_empty = kv_full + kRing;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kv_empty + kRing);
+  uint64_t* kv_full = bars + 2;   // [kRing]
+  uint64_t* kv_empty = bars + 5;  // [kRing]
+  uint64_t* s_full = bars + 8;    // [2 tiles]
+  uint64_t* s_free = bars + 10;   // [2]
+  uint64_t* p_full = bars + 12;   // [2]
+  uint64_t* p_free = bars + 14;   // [2]
+  uint64_t* o_empty = bars + 16;  // [2]
+  uint64_t* drain = bars + 18;    // [2 issuers]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  FirstWalk* first = reinterpret_cast<FirstWalk*>(bars + 40);
-  static_assert(16 + 2 * kRing + 1 <= 40 && 40 * 8 + sizeof(FirstWalk) <= 512, "barrier area");
+  FirstWalk* first = reinterpret_cast<FirstWalk*>(bars + 24);
+  static_assert(24 * 8 + sizeof(FirstWalk) <= 512, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -260,15 +261,15 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 2);
     }
-    for (int w = 0; w < 4; ++w) {
-      mbar_init(&s_full[w], 1);
-      mbar_init(&p_full[w], 4);
-    }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&pv_done[w], 1);
-      mbar_init(&o_full[w], 1);
-      mbar_init(&drain[w], 1);
+      mbar_init(&s_full[w], 1);
+      mbar_init(&s_free[w], 4);
+      mbar_init(&p_full[w], 4);
+      mbar_init(&p_free[w], 1);
+      mbar_init(&o_empty[w], 4);
     }
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     *abort_flag = 0u;
     fence_barrier_init();
   }
@@ -293,16 +294,17 @@ __global__ void __launch_bounds__(384, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // registers: 128 threads x 104 and 256 x 200 are the launch's 384 x 168
+  if (warp < 4) {
+    regs_dealloc<104>();
+    if (warp == 0 && lane == 0) {
       // ------------------------------------------------------------------ producer
-      // K(t), V(t) of every step in turn; a segment's Q tiles before its first K.
+      // Per step t, K(t) then V(t - 1); at a segment's first step (not the walk's first)
+      // V(t - 1) goes first.  A segment's Q tiles go before its first K.
       bool ok = true;
       int slot = 0;
       uint32_t ring_phase = 0;
-      int armed[kRing];
-#pragma unroll
-      for (int s = 0; s < kRing; ++s) armed[s] = -1;
+      int armed[kRing] = {-1, -1, -1};
       int q_armed = -1;
       auto load = [&](bool is_v, const Unit& u, int j) -> bool {
         if (!wait_soon(&kv_empty[slot], ring_phase ^ 1u, abort_flag, a.err, kErrAttnWait))
@@ -315,55 +317,62 @@ __global__ void __launch_bounds__(384, 1)
         for (int x = 0; x < Cfg::kNBox; ++x)
           tma_load_4d(sKV + slot * Cfg::kTile + x * kBox, m, &kv_full[slot], 64 * x, tok,
                       u.h / a.group, far ? 0 : u.b);
-#pragma unroll
-        for (int s = 0; s < kRing; ++s)
-          if (s == slot) armed[s] = static_cast<int>(ring_phase);
+        armed[slot] = static_cast<int>(ring_phase);
         if (++slot == kRing) {
           slot = 0;
           ring_phase ^= 1u;
         }
         return true;
       };
-      int n = 0;
-      for (Walk w = first->walk; w.more && ok; w.next(a), ++n) {
-        if (n > 0 && !wait_soon(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, a.err,
-                                kErrAttnWait)) {
-          ok = false;
-          break;
+      Walk w = first->walk;
+      Unit pu{};          // the step before's
+      int pj = -1, n = 0;
+      while (w.more && ok) {
+        if (pj >= 0) ok = load(true, pu, pj);
+        for (int j = w.j0; j < w.j1 && ok; ++j) {
+          if (j == w.j0) {
+            if (n > 0 && !wait_soon(q_empty, static_cast<uint32_t>(n - 1) & 1u, abort_flag, a.err,
+                                   kErrAttnWait)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(q_full, 2 * Cfg::kTile);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int x = 0; x < Cfg::kNBox; ++x)
+                tma_load_4d(sQ + t * Cfg::kTile + x * kBox, &tm.q, q_full, 64 * x,
+                            w.u.qb * kBlockQ + t * 128, w.u.h, w.u.b);
+            q_armed = n & 1;
+          }
+          ok = load(false, w.u, j) && (j == w.j0 || load(true, w.u, j - 1));
         }
-        mbar_arrive_expect_tx(q_full, 2 * Cfg::kTile);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int x = 0; x < Cfg::kNBox; ++x)
-            tma_load_4d(sQ + t * Cfg::kTile + x * kBox, &tm.q, q_full, 64 * x,
-                        w.u.qb * kBlockQ + t * 128, w.u.h, w.u.b);
-        q_armed = n & 1;
-        for (int j = w.j0; j < w.j1 && ok; ++j) ok = load(false, w.u, j) && load(true, w.u, j);
+        pu = w.u;
+        pj = w.j1 - 1;
+        ++n;
+        w.next(a);
       }
+      if (ok && pj >= 0) ok = load(true, pu, pj);
       if (!ok) {
         if (q_armed >= 0) drain_wait(q_full, static_cast<uint32_t>(q_armed));
-#pragma unroll
         for (int s = 0; s < kRing; ++s)
           if (armed[s] >= 0) drain_wait(&kv_full[s], static_cast<uint32_t>(armed[s]));
       }
-    }
-  } else if (warp == 1 || warp == 2) {
-    if (lane == 0) {
+    } else if ((warp == 1 || warp == 2) && lane == 0) {
       // ------------------------------------------------------------------ MMA issuers
-      // Per step t of tile w: P V of half 0, S of the next step's half 0, and the same of half
-      // 1.  S of a half overwrites the weights that P V before it reads: the tensor core takes a
-      // thread's products in order.
       const int w = warp - 1;
       int slot = 0;
       uint32_t ring_phase = 0;
-      uint32_t pvc = 0;  // steps of this tile whose P V was issued
+      int cnt = 0, pvc = 0;  // S and P V products issued for this tile
+      int units = 0;         // segments whose last P V was issued (tile present)
+      int n = 0;
       const uint64_t q_desc = opaque_u64(sdesc_sw128(smem_u32(sQ + w * Cfg::kTile), 16, 1024));
+      const uint64_t p_desc = opaque_u64(sdesc_sw128(smem_u32(sP + w * Cfg::kPBytes), 16, 1024));
       const uint64_t k_desc0 = opaque_u64(sdesc_sw128(smem_u32(sKV), 16, 1024));
       const uint64_t v_desc0 = opaque_u64(sdesc_sw128(smem_u32(sKV), kBox, 1024));
       const uint32_t s_tmem = tmem + w * 128;
       const uint32_t o_tmem = tmem + kOCol + w * 128;
-      auto take = [&](int& s_out) -> bool {
+      auto ring_take = [&](int& s_out) -> bool {
         if (!wait_soon(&kv_full[slot], ring_phase, abort_flag, a.err, kErrAttnWait)) return false;
         s_out = slot;
         if (++slot == kRing) {
@@ -372,73 +381,72 @@ __global__ void __launch_bounds__(384, 1)
         }
         return true;
       };
-      auto issue_s = [&](int ks, int h) {
-        const uint64_t k_desc = k_desc0 + static_cast<uint64_t>(ks) * (Cfg::kTile >> 4) + h * 512;
-        if constexpr (HD == 128)
-          umma_f16_x8_kk<kBox / 16>(s_tmem + h * 64, q_desc, k_desc, IDESC_S, 0u);
-        else
-          umma_f16_x4_kk(s_tmem + h * 64, q_desc, k_desc, IDESC_S, 0u);
-        tc_commit(&s_full[w * 2 + h]);
-      };
-      bool ok = true;
-      int n = 0;
-      for (Walk wk = first->walk; wk.more && ok; wk.next(a), ++n) {
-        const bool here = w == 0 || wk.u.qb * kBlockQ + 128 < wk.u.len.q;
-        int ks = 0, vs = 0;
-        if (!wait_soon(q_full, static_cast<uint32_t>(n) & 1u, abort_flag, a.err, kErrAttnWait) ||
-            !take(ks))
-          break;
+      auto issue_s = [&](bool here, bool first, bool last) -> bool {
+        if (first &&
+            !wait_soon(q_full, static_cast<uint32_t>(n) & 1u, abort_flag, a.err, kErrAttnWait))
+          return false;
+        int ksl;
+        if (!ring_take(ksl)) return false;
         if (here) {
+          if (cnt >= 1 && !wait_soon(&s_free[w], static_cast<uint32_t>(cnt - 1) & 1u, abort_flag,
+                                    a.err, kErrAttnWait))
+            return false;
           tc_fence_after();
-          issue_s(ks, 0);
-          issue_s(ks, 1);
+          const uint64_t k_desc = k_desc0 + static_cast<uint64_t>(ksl) * (Cfg::kTile >> 4);
+          if constexpr (HD == 128)
+            umma_f16_x8_kk<kBox / 16>(s_tmem, q_desc, k_desc, IDESC_S, 0u);
+          else
+            umma_f16_x4_kk(s_tmem, q_desc, k_desc, IDESC_S, 0u);
+          tc_commit(&s_full[w]);
+          ++cnt;
         }
-        tc_commit(&kv_empty[ks]);
-        if (wk.j1 - wk.j0 == 1) tc_commit(q_empty);
-        for (int j = wk.j0; j < wk.j1; ++j) {
-          const bool more = j + 1 < wk.j1;
-          if (!take(vs) || (more && !here && !take(ks))) {
-            ok = false;
-            break;
-          }
-          if (here) {
-            const uint64_t v_desc = v_desc0 + static_cast<uint64_t>(vs) * (Cfg::kTile >> 4);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (!wait_soon(&p_full[w * 2 + h], pvc & 1u, abort_flag, a.err, kErrAttnWait)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma_f16_ts(o_tmem, s_tmem + h * 64 + kk * 8, v_desc + (h * 4 + kk) * 128, IDESC_PV,
-                            (j > wk.j0 || h > 0 || kk > 0) ? 1u : 0u);
-              tc_commit(&pv_done[w]);
-              if (more) {
-                if (h == 0 && !take(ks)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                issue_s(ks, h);
-              }
-            }
-            if (!ok) break;
-            ++pvc;
-            if (!more) tc_commit(&o_full[w]);
-          }
-          tc_commit(&kv_empty[vs]);
-          if (more) {
-            tc_commit(&kv_empty[ks]);
-            if (j + 2 == wk.j1) tc_commit(q_empty);
-          }
+        tc_commit(&kv_empty[ksl]);
+        if (last) tc_commit(q_empty);
+        return true;
+      };
+      auto issue_pv = [&](bool here, bool first, bool last) -> bool {
+        int vsl;
+        if (!ring_take(vsl)) return false;
+        if (here) {
+          // the tile's previous segment must have read O out before it is overwritten
+          if (first && units > 0 &&
+              !wait_soon(&o_empty[w], static_cast<uint32_t>(units - 1) & 1u, abort_flag, a.err,
+                        kErrAttnWait))
+            return false;
+          if (!wait_soon(&p_full[w], static_cast<uint32_t>(pvc) & 1u, abort_flag, a.err,
+                        kErrAttnWait))
+            return false;
+          tc_fence_after();
+          umma_f16_x8_kmn<kBox / 16>(
+              o_tmem, p_desc, v_desc0 + static_cast<uint64_t>(vsl) * (Cfg::kTile >> 4), IDESC_PV,
+              first ? 0u : 1u);
+          tc_commit(&p_free[w]);
+          ++pvc;
+          if (last) ++units;
         }
+        tc_commit(&kv_empty[vsl]);
+        return true;
+      };
+      Walk wk = first->walk;
+      bool ok = true, p_here = false, p_first = false, pending = false;
+      while (wk.more && ok) {
+        const bool here = w == 0 || wk.u.qb * kBlockQ + 128 < wk.u.len.q;
+        if (pending) ok = issue_pv(p_here, p_first, true);
+        for (int j = wk.j0; j < wk.j1 && ok; ++j)
+          ok = issue_s(here, j == wk.j0, j + 1 == wk.j1) &&
+               (j == wk.j0 || issue_pv(here, j - 1 == wk.j0, false));
+        pending = true;
+        p_here = here;
+        p_first = wk.j1 - 1 == wk.j0;
+        ++n;
+        wk.next(a);
       }
+      if (ok && pending) issue_pv(p_here, p_first, true);
       tc_commit(&drain[w]);
       drain_wait(&drain[w], 0);
     }
-  } else if (warp >= 4) {
+  } else {
+    regs_alloc<200>();
     // ------------------------------------------------------------------ softmax (tile w)
     const int w = (warp - 4) >> 2;
     const int quarter = warp & 3;
@@ -447,10 +455,10 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t s_addr = tmem + lane_addr + w * 128;
     const uint32_t o_addr = tmem + lane_addr + kOCol + w * 128;
     const float sl2 = a.scale_log2;
+    uint8_t* pbuf = sP + w * Cfg::kPBytes + row * 128;
     bool ok = true;
-    uint32_t c = 0;     // steps of this tile so far
-    uint32_t t = 0;     // steps of this CTA so far (ring position: V of step t is load 2 t + 1)
-    uint32_t ends = 0;  // segments of this tile so far
+    int c = 0;  // steps of this tile so far
+    int t = 0;  // steps of this CTA so far (ring position)
     for (Walk wk = first->walk; wk.more && ok; wk.next(a)) {
       const int q0 = wk.u.qb * kBlockQ + w * 128;
       if (w == 1 && q0 >= wk.u.len.q) {
@@ -461,67 +469,78 @@ __global__ void __launch_bounds__(384, 1)
       int own_end = wk.u.len.kv;
       if (a.causal) own_end = min(own_end, q0 + row + 1 + wk.u.len.kv - wk.u.len.q);
       float m = -INFINITY, l = 0.f;
-      for (int j = wk.j0; j < wk.j1 && ok; ++j, ++c, ++t) {
+      for (int j = wk.j0; j < wk.j1; ++j, ++c, ++t) {
+        ok = warp_wait(&s_full[w], static_cast<uint32_t>(c) & 1u, abort_flag,
+                                              a.err, kErrAttnWait);
+        if (!ok) break;
+        tc_fence_after();
+        float s[128];
+        {
+          uint32_t r[128];
+          tmem_ld128_sync(s_addr, r);
+#pragma unroll
+          for (int q = 0; q < 128; ++q) s[q] = __uint_as_float(r[q]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[w]);
         const bool far = j < a.prefix_tiles;
         const int tok = (far ? j : j - a.prefix_tiles) * 128;
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          ok = warp_wait(&s_full[w * 2 + h], c & 1u, abort_flag, a.err, kErrAttnWait);
+        const int lim = (far ? a.n_prefix : own_end) - tok;
+        const float alpha = softmax_max(s, lim, sl2, m);
+        uint32_t pk[64];
+        softmax_exp<T>(s, sl2, m, alpha, l, pk);
+        if (c >= 1) {
+          // the P tile is free, and O complete, once the tile's previous P V has finished
+          ok = warp_wait(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
+                                                abort_flag, a.err, kErrAttnWait);
           if (!ok) break;
+        }
+#pragma unroll
+        for (int c16 = 0; c16 < 16; ++c16) {
+          const int chunk = (c16 & 7) ^ (row & 7);
+          *reinterpret_cast<uint4*>(pbuf + (c16 >> 3) * kBox + chunk * 16) =
+              make_uint4(pk[c16 * 4], pk[c16 * 4 + 1], pk[c16 * 4 + 2], pk[c16 * 4 + 3]);
+        }
+        if (j > wk.j0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
           tc_fence_after();
-          float s[64];
-          {
-            uint32_t r[64];
-            tmem_ld64_sync(s_addr + h * 64, r);
-#pragma unroll
-            for (int q = 0; q < 64; ++q) s[q] = __uint_as_float(r[q]);
-          }
-          const float alpha =
-              softmax_max(s, (far ? a.n_prefix : own_end) - tok - h * 64, sl2, m);
-          uint32_t pk[32];
-          softmax_exp<T>(s, sl2, m, alpha, l, pk);
-          tmem_st32(s_addr + h * 64, pk);
-          if ((j > wk.j0 || h > 0) && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            // O holds every earlier product once the half before this one's is done (those
-            // before that one are: this half's S was issued behind them)
-            ok = warp_wait(&pv_done[w], (2 * c + h - 1) & 1u, abort_flag, a.err, kErrAttnWait);
-            if (!ok) break;
-            tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < HD / 32; ++cc) {
-              uint32_t r[32];
-              tmem_ld32(o_addr + cc * 32, r);
-              tmem_wait_ld(r);
+          for (int cc = 0; cc < HD / 32; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(o_addr + cc * 32, r);
+            tmem_wait_ld(r);
 #pragma unroll
-              for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha);
-              tmem_st32(o_addr + cc * 32, r);
-            }
+            for (int q = 0; q < 32; ++q) r[q] = __float_as_uint(__uint_as_float(r[q]) * alpha);
+            tmem_st32(o_addr + cc * 32, r);
           }
           tmem_wait_st();
-          if (h == 0 && !far && wk.u.len.kv - tok < 128) {
-            // the values behind the sequence's end may be anything (0 * NaN is NaN): zeros, of
-            // both halves, before the first of them is released
-            const int vs = (2 * t + 1) % kRing;
-            ok = warp_wait(&kv_full[vs], ((2 * t + 1) / kRing) & 1u, abort_flag, a.err, kErrAttnWait);
-            if (!ok) break;
-            const int from = max(0, wk.u.len.kv - tok);
-            uint4* v = reinterpret_cast<uint4*>(sKV + vs * Cfg::kTile);
-            for (int i = row; i < (128 - from) * 8 * Cfg::kNBox; i += 128) {
-              const int x = i / ((128 - from) * 8), e = i - x * (128 - from) * 8;
-              v[x * (kBox / 16) + from * 8 + e] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[w * 2 + h]);
         }
+        if (!far && wk.u.len.kv - tok < 128) {
+          // the values behind the sequence's end may be anything (0 * NaN is NaN): zeros.  V
+          // of step t is the ring's load 2 t + 2, or 2 t + 1 at a segment's last step.
+          const int idx = 2 * t + (j + 1 == wk.j1 ? 1 : 2);
+          const int vsl = idx % kRing;
+          ok = warp_wait(&kv_full[vsl], static_cast<uint32_t>(idx / kRing) & 1u,
+                                   abort_flag, a.err, kErrAttnWait);
+          if (!ok) break;
+          const int from = max(0, wk.u.len.kv - tok);
+          uint4* v = reinterpret_cast<uint4*>(sKV + vsl * Cfg::kTile);
+          for (int i = row; i < (128 - from) * 8 * Cfg::kNBox; i += 128) {
+            const int x = i / ((128 - from) * 8), e = i - x * (128 - from) * 8;
+            v[x * (kBox / 16) + from * 8 + e] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          // all four warps' zeros before any of them releases P: the product reads all rows
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
       }
       if (!ok) break;
       // ---- end of the segment: O holds every P V product once the last one completes
-      ok = warp_wait(&o_full[w], ends & 1u, abort_flag, a.err, kErrAttnWait);
+      ok = warp_wait(&p_free[w], static_cast<uint32_t>(c - 1) & 1u,
+                                            abort_flag, a.err, kErrAttnWait);
       if (!ok) break;
-      ++ends;
       tc_fence_after();
       const int part = static_cast<int>(blockIdx.x) * 2 + w;
       if (wk.j1 < wk.u.steps) {
@@ -568,56 +587,52 @@ __global__ void __launch_bounds__(384, 1)
           m = top;
         }
         const float inv_l = m == -INFINITY ? 0.0f : 1.0f / l;  // 0: the row sees no key
-        // 64 channels at a time through shared memory, rotated by the row, so that the stores are
-        // whole lines: the warp's own 32 rows, those past q_len left out
-        uint4* stage = reinterpret_cast<uint4*>(sOut + w * kBox);
+        constexpr int kVecs = HD / 8;  // 16-byte pieces of a row
+        uint4* stage = reinterpret_cast<uint4*>(sP + w * Cfg::kPBytes);
+#pragma unroll 1
+        for (int cc = 0; cc < HD / 32; ++cc) {
+          float o[32];
+          {
+            uint32_t r[32];
+            tmem_ld32(o_addr + cc * 32, r);
+            tmem_wait_ld(r);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(r[q]) * wb;
+          }
+          for (int from = lo; from < me; ++from) {
+            if (!has_piece(wk.u, all, from)) continue;
+            const int src = from * 2 + w;
+            const float wa = weight_of(__ldcg(a.part_ml + size_t(src) * 128 + row).x, m);
+            const float4* po = a.part_o + size_t(src) * (HD / 4) * 128 + row;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = __ldcg(po + size_t(cc * 8 + i) * 128);
+              o[4 * i + 0] = fmaf(v.x, wa, o[4 * i + 0]);
+              o[4 * i + 1] = fmaf(v.y, wa, o[4 * i + 1]);
+              o[4 * i + 2] = fmaf(v.z, wa, o[4 * i + 2]);
+              o[4 * i + 3] = fmaf(v.w, wa, o[4 * i + 3]);
+            }
+          }
+          // to this row of the P tile, which is free: 16 bytes at a time, rotated by the row
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint4 u;
+            u.x = pack2<T>(o[8 * i + 0] * inv_l, o[8 * i + 1] * inv_l);
+            u.y = pack2<T>(o[8 * i + 2] * inv_l, o[8 * i + 3] * inv_l);
+            u.z = pack2<T>(o[8 * i + 4] * inv_l, o[8 * i + 5] * inv_l);
+            u.w = pack2<T>(o[8 * i + 6] * inv_l, o[8 * i + 7] * inv_l);
+            stage[row * kVecs + ((cc * 4 + i + row) & (kVecs - 1))] = u;
+          }
+        }
+        // and from there whole rows at a time: the warp's own 32, those past q_len left out
+        __syncwarp();
         T* dst = static_cast<T*>(a.out.data) + wk.u.b * a.out.batch + wk.u.h * a.out.head;
-#pragma unroll 1
-        for (int half = 0; half < HD / 64; ++half) {
-#pragma unroll 1
-          for (int cc = 2 * half; cc < 2 * half + 2; ++cc) {
-            float o[32];
-            {
-              uint32_t r[32];
-              tmem_ld32(o_addr + cc * 32, r);
-              tmem_wait_ld(r);
-#pragma unroll
-              for (int q = 0; q < 32; ++q) o[q] = __uint_as_float(r[q]) * wb;
-            }
-            for (int from = lo; from < me; ++from) {
-              if (!has_piece(wk.u, all, from)) continue;
-              const int src = from * 2 + w;
-              const float wa = weight_of(__ldcg(a.part_ml + size_t(src) * 128 + row).x, m);
-              const float4* po = a.part_o + size_t(src) * (HD / 4) * 128 + row;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 v = __ldcg(po + size_t(cc * 8 + i) * 128);
-                o[4 * i + 0] = fmaf(v.x, wa, o[4 * i + 0]);
-                o[4 * i + 1] = fmaf(v.y, wa, o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(v.z, wa, o[4 * i + 2]);
-                o[4 * i + 3] = fmaf(v.w, wa, o[4 * i + 3]);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 u;
-              u.x = pack2<T>(o[8 * i + 0] * inv_l, o[8 * i + 1] * inv_l);
-              u.y = pack2<T>(o[8 * i + 2] * inv_l, o[8 * i + 3] * inv_l);
-              u.z = pack2<T>(o[8 * i + 4] * inv_l, o[8 * i + 5] * inv_l);
-              u.w = pack2<T>(o[8 * i + 6] * inv_l, o[8 * i + 7] * inv_l);
-              stage[row * 8 + (((cc & 1) * 4 + i + row) & 7)] = u;
-            }
-          }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = quarter * 32 + i * 4 + (lane >> 3), v = lane & 7;
-            const uint4 u = stage[r * 8 + ((v + r) & 7)];
-            if (q0 + r < wk.u.len.q)
-              *reinterpret_cast<uint4*>(dst + static_cast<long long>(q0 + r) * a.out.token + half * 64 +
-                                        v * 8) = u;
-          }
-          __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kVecs; ++i) {
+          const int r = quarter * 32 + (i * 32 + lane) / kVecs, v = lane & (kVecs - 1);
+          const uint4 u = stage[r * kVecs + ((v + r) & (kVecs - 1))];
+          if (q0 + r < wk.u.len.q)
+            *reinterpret_cast<uint4*>(dst + static_cast<long long>(q0 + r) * a.out.token + v * 8) = u;
         }
         // the flags go back at zero, so that a replay of this launch waits for them again
         __syncwarp();
@@ -625,8 +640,10 @@ __global__ void __launch_bounds__(384, 1)
           for (int from = lo; from < me; ++from)
             if (has_piece(wk.u, all, from)) a.flags[(from * 2 + w) * 4 + quarter] = 0ull;
       }
-      // (the next segment's first P V, which overwrites O, waits for weights stored after this)
+      // O may now be overwritten by the next segment's first P V
       tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_empty[w]);
     }
   }
 
