@@ -13,11 +13,11 @@
 //
 // What bounds it: HBM.  Forward reads and writes every head once, backward reads x and gy
 // and writes dx.  So a warp takes a token and walks over its heads of q or of k (a block has
-// one or the other, which keeps one set of gains and sums in registers): each lane owns eight
-// channels of a head (the four pairs 4 s .. 4 s + 3 of its slot s, in both pairings), so the
+// one or the other, which keeps one set of gains and sums in registers): each lane owns 16 or 8
+// channels of a head (the pairs C/2 s .. C/2 s + C/2 - 1 of its slot s, in both pairings), so the
 // angles of a token are computed once for all heads of the warp's item, pairs never cross
-// lanes, and the only shuffles are those of the norm's sums.  An item's first loads are issued
-// before its angles are computed, later ones while the heads before them are worked on.
+// lanes, and the only shuffles are those of the norm's sums and the angles'.  A group of heads is
+// loaded while the one before it is worked on, from one item into the next.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -33,17 +33,19 @@ constexpr int kWarps = 4;  // warps of a block
 
 enum Mode : int { kModeRope = 0, kModeNorm = 1, kModeNormBwd = 2 };
 
-// A lane's eight channels: chunk c0 .. c0 + 3 and chunk c1 .. c1 + 3.  Adjacent pairing:
-// c1 = c0 + 4 and pair i is (f[2 i], f[2 i + 1]).  Half-split pairing: c1 = c0 + rot / 2 and
-// pair i is (f[i], f[4 + i]); behind the rotated width c1 = c0 + 4.
-template <typename T>
+// A lane's C channels (C / 2 pairs): chunk c0 .. c0 + C/2 - 1 and chunk c1 .. c1 + C/2 - 1.
+// Adjacent pairing: c1 = c0 + C/2 and pair i is channels (2 i, 2 i + 1) of the two laid end to
+// end.  Half-split pairing: c1 = c0 + rot / 2 and pair i is (c0 + i, c1 + i); behind the rotated
+// width c1 = c0 + C/2.  C = 16 (16-bit types, widths that are multiples of 16) makes both chunks
+// 16-byte accesses and halves the shuffles, roots and addresses per byte; C = 8 is for the rest.
+template <typename T, int C>
 struct Raw {
-  uint32_t w[2 * sizeof(T)];
+  uint32_t w[C * sizeof(T) / 4];
 };
 
-template <typename T, bool HALVES>
-__device__ __forceinline__ void load_raw(const T* p, int c0, int c1, Raw<T>& r) {
-  if constexpr (sizeof(T) == 4) {
+template <typename T, int C, bool HALVES>
+__device__ __forceinline__ void load_raw(const T* p, int c0, int c1, Raw<T, C>& r) {
+  if constexpr (C * sizeof(T) == 32) {  // two chunks of 16 bytes
     const uint4 a = *reinterpret_cast<const uint4*>(p + c0);
     const uint4 b = *reinterpret_cast<const uint4*>(p + c1);
     r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
@@ -58,9 +60,9 @@ __device__ __forceinline__ void load_raw(const T* p, int c0, int c1, Raw<T>& r) 
   }
 }
 
-template <typename T, bool HALVES>
-__device__ __forceinline__ void store_raw(T* p, int c0, int c1, const Raw<T>& r) {
-  if constexpr (sizeof(T) == 4) {
+template <typename T, int C, bool HALVES>
+__device__ __forceinline__ void store_raw(T* p, int c0, int c1, const Raw<T, C>& r) {
+  if constexpr (C * sizeof(T) == 32) {
     *reinterpret_cast<uint4*>(p + c0) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     *reinterpret_cast<uint4*>(p + c1) = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
   } else if constexpr (HALVES) {
@@ -71,11 +73,12 @@ __device__ __forceinline__ void store_raw(T* p, int c0, int c1, const Raw<T>& r)
   }
 }
 
-// The four pairs of a lane, members a and b apart, as packed fp32: a[0] holds pairs 0 and 1.
+// The pairs of a lane, members a and b apart, as packed fp32: a[0] holds pairs 0 and 1.
 // Packed arithmetic does two of them in one issue slot, which is what these kernels run out of
 // first once enough loads are in flight.
+template <int C>
 struct Pairs {
-  uint64_t a[2], b[2];
+  uint64_t a[C / 4], b[C / 4];
 };
 
 template <typename T>
@@ -90,20 +93,21 @@ __device__ __forceinline__ uint32_t two(float x, float y) {
   else return pack_bf16x2(x, y);
 }
 
-template <typename T, bool HALVES>
-__device__ __forceinline__ Pairs widen(const Raw<T>& r) {
-  Pairs p;
+template <typename T, int C, bool HALVES>
+__device__ __forceinline__ Pairs<C> widen(const Raw<T, C>& r) {
+  Pairs<C> p;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < C / 4; ++i) {
     if constexpr (std::is_same_v<T, float>) {
       const float f0 = __uint_as_float(r.w[HALVES ? 2 * i : 4 * i]);
       const float f1 = __uint_as_float(r.w[HALVES ? 2 * i + 1 : 4 * i + 1]);
-      const float f2 = __uint_as_float(r.w[HALVES ? 4 + 2 * i : 4 * i + 2]);
-      const float f3 = __uint_as_float(r.w[HALVES ? 5 + 2 * i : 4 * i + 3]);
+      const float f2 = __uint_as_float(r.w[HALVES ? C / 2 + 2 * i : 4 * i + 2]);
+      const float f3 = __uint_as_float(r.w[HALVES ? C / 2 + 1 + 2 * i : 4 * i + 3]);
       p.a[i] = HALVES ? pack_f32x2(f0, f1) : pack_f32x2(f0, f2);
       p.b[i] = HALVES ? pack_f32x2(f2, f3) : pack_f32x2(f1, f3);
     } else {
-      const float2 u = two<T>(r.w[HALVES ? i : 2 * i]), v = two<T>(r.w[HALVES ? 2 + i : 2 * i + 1]);
+      const float2 u = two<T>(r.w[HALVES ? i : 2 * i]);
+      const float2 v = two<T>(r.w[HALVES ? C / 4 + i : 2 * i + 1]);
       p.a[i] = HALVES ? pack_f32x2(u.x, u.y) : pack_f32x2(u.x, v.x);
       p.b[i] = HALVES ? pack_f32x2(v.x, v.y) : pack_f32x2(u.y, v.y);
     }
@@ -111,40 +115,46 @@ __device__ __forceinline__ Pairs widen(const Raw<T>& r) {
   return p;
 }
 
-template <typename T, bool HALVES>
-__device__ __forceinline__ Raw<T> narrow(const Pairs& p) {
-  Raw<T> r;
+template <typename T, int C, bool HALVES>
+__device__ __forceinline__ Raw<T, C> narrow(const Pairs<C>& p) {
+  Raw<T, C> r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < C / 4; ++i) {
     float a0, a1, b0, b1;
     unpack_f32x2(p.a[i], a0, a1);
     unpack_f32x2(p.b[i], b0, b1);
     if constexpr (std::is_same_v<T, float>) {
       r.w[HALVES ? 2 * i : 4 * i] = __float_as_uint(a0);
       r.w[HALVES ? 2 * i + 1 : 4 * i + 2] = __float_as_uint(a1);
-      r.w[HALVES ? 4 + 2 * i : 4 * i + 1] = __float_as_uint(b0);
-      r.w[HALVES ? 5 + 2 * i : 4 * i + 3] = __float_as_uint(b1);
+      r.w[HALVES ? C / 2 + 2 * i : 4 * i + 1] = __float_as_uint(b0);
+      r.w[HALVES ? C / 2 + 1 + 2 * i : 4 * i + 3] = __float_as_uint(b1);
     } else {
       r.w[HALVES ? i : 2 * i] = HALVES ? two<T>(a0, a1) : two<T>(a0, b0);
-      r.w[HALVES ? 2 + i : 2 * i + 1] = HALVES ? two<T>(b0, b1) : two<T>(a1, b1);
+      r.w[HALVES ? C / 4 + i : 2 * i + 1] = HALVES ? two<T>(b0, b1) : two<T>(a1, b1);
     }
   }
   return r;
 }
 
-__device__ __forceinline__ Pairs mul(const Pairs& p, uint64_t f) {
-  Pairs r;
+template <int C>
+__device__ __forceinline__ Pairs<C> mul(const Pairs<C>& p, uint64_t f) {
+  Pairs<C> r;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < C / 4; ++i) {
     r.a[i] = mul_f32x2(p.a[i], f);
     r.b[i] = mul_f32x2(p.b[i], f);
   }
   return r;
 }
-// sum of the products of the eight channels
-__device__ __forceinline__ float dot8(const Pairs& p, const Pairs& q) {
-  const uint64_t x = fma_f32x2(p.a[0], q.a[0], mul_f32x2(p.b[0], q.b[0]));
-  const uint64_t y = fma_f32x2(p.a[1], q.a[1], mul_f32x2(p.b[1], q.b[1]));
+// sum of the products of the channels
+template <int C>
+__device__ __forceinline__ float dot(const Pairs<C>& p, const Pairs<C>& q) {
+  uint64_t x = mul_f32x2(p.a[0], q.a[0]), y = mul_f32x2(p.b[0], q.b[0]);
+#pragma unroll
+  for (int i = 1; i < C / 4; ++i) {
+    x = fma_f32x2(p.a[i], q.a[i], x);
+    y = fma_f32x2(p.b[i], q.b[i], y);
+  }
   float lo, hi;
   unpack_f32x2(add_f32x2(x, y), lo, hi);
   return lo + hi;
@@ -158,14 +168,45 @@ __device__ __forceinline__ void sincos_turns(double t, float& s, float& c) {
 }
 
 // A turn, with a factor on each member before it (the gains): a -> a ac - b bs, b -> a as + b bc.
+template <int C>
 struct Turn {
-  uint64_t ac[2], nbs[2], as[2], bc[2];  // nbs = -bs
+  uint64_t ac[C / 4], nbs[C / 4], as[C / 4], bc[C / 4];  // nbs = -bs
 };
 
-__device__ __forceinline__ Pairs rotate(const Pairs& p, const Turn& t) {
-  Pairs r;
+// Kept in shared memory, 16 bytes of every lane side by side: in registers the turn would cost
+// a quarter of the warps.
+template <int C>
+__device__ __forceinline__ void put(uint4* at, int part, const uint64_t (&v)[C / 4]) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < C / 8; ++i)
+    *reinterpret_cast<ulonglong2*>(at + (part * (C / 8) + i) * kWarps * 32) =
+        make_ulonglong2(v[2 * i], v[2 * i + 1]);
+}
+template <int C>
+__device__ __forceinline__ void get(const uint4* at, int part, uint64_t (&v)[C / 4]) {
+#pragma unroll
+  for (int i = 0; i < C / 8; ++i) {
+    const ulonglong2 u =
+        *reinterpret_cast<const ulonglong2*>(at + (part * (C / 8) + i) * kWarps * 32);
+    v[2 * i] = u.x;
+    v[2 * i + 1] = u.y;
+  }
+}
+template <int C>
+__device__ __forceinline__ Turn<C> load_turn(const uint4* at) {
+  Turn<C> t;
+  get<C>(at, 0, t.ac);
+  get<C>(at, 1, t.nbs);
+  get<C>(at, 2, t.as);
+  get<C>(at, 3, t.bc);
+  return t;
+}
+
+template <int C>
+__device__ __forceinline__ Pairs<C> rotate(const Pairs<C>& p, const Turn<C>& t) {
+  Pairs<C> r;
+#pragma unroll
+  for (int i = 0; i < C / 4; ++i) {
     r.a[i] = fma_f32x2(p.a[i], t.ac[i], mul_f32x2(p.b[i], t.nbs[i]));
     r.b[i] = fma_f32x2(p.a[i], t.as[i], mul_f32x2(p.b[i], t.bc[i]));
   }
@@ -180,46 +221,48 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// Channel of pair i's members behind the first of a lane's eight contiguous ones.
-template <bool HALVES>
+// Channel of pair i's members behind the first of a lane's contiguous ones.
+template <int C, bool HALVES>
 __device__ __forceinline__ constexpr int member_a(int i) {
   return HALVES ? i : 2 * i;
 }
-template <bool HALVES>
+template <int C, bool HALVES>
 __device__ __forceinline__ constexpr int member_b(int i) {
-  return HALVES ? 4 + i : 2 * i + 1;
+  return HALVES ? C / 2 + i : 2 * i + 1;
 }
 
 // A group is kPass passes of 32 / LPH heads.  An item is one token, or (parts > 1, where
 // tokens are few) an equal share of its groups.
-template <typename T, int MODE>
+template <typename T, int C, int MODE>
 constexpr int pass_count() {
-  return (MODE == kModeNormBwd || sizeof(T) == 4) ? 1 : 2;
+  return (MODE == kModeNormBwd || C * sizeof(T) == 32) ? 1 : 2;
 }
 
 // What an item costs beside its groups of heads (its angles, and its first loads' latency), in
 // groups.
 constexpr int kItemCost = 1;
 
-// Blocks that are on an SM at a time (their registers: 64, 80 and 96 a thread); the grid is
-// that many a SM at most.
-constexpr int blocks_per_sm(int mode) {
-  return mode == kModeNormBwd ? kHeadRowsBwdPerSm : mode == kModeNorm ? 6 : 8;
+// Blocks that are on an SM at a time; the grid is that many a SM at most.
+constexpr int blocks_per_sm(int mode, int C) {
+  if (mode == kModeRope) return 8;
+  if (mode == kModeNorm) return C == 16 ? 5 : 6;
+  return C == 16 ? 4 : 5;
 }
 
-template <typename T, bool HALVES, int LPH, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(const __grid_constant__ HeadRows a) {
-  constexpr int kPass = pass_count<T, MODE>();
+template <typename T, int C, bool HALVES, int LPH, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_rows(const __grid_constant__ HeadRows a) {
+  constexpr int kPass = pass_count<T, C, MODE>();
   constexpr int kHeads = 32 / LPH;
   constexpr int kGroup = kPass * kHeads;
   constexpr bool kBwd = MODE == kModeNormBwd;
   const int lane = threadIdx.x & 31;
   const int slot = lane % LPH, sub = lane / LPH;
-  const bool live = slot * 8 < a.head_dim;
-  const bool turned = slot * 4 < a.n_pairs;
+  constexpr int kPairs = C / 2;
+  const bool live = slot * C < a.head_dim;
+  const bool turned = slot * kPairs < a.n_pairs;
   const bool half_slot = HALVES && turned;
-  const int c0 = half_slot ? slot * 4 : slot * 8;
-  const int c1 = half_slot ? a.n_pairs + slot * 4 : slot * 8 + 4;
+  const int c0 = half_slot ? slot * kPairs : slot * C;
+  const int c1 = half_slot ? a.n_pairs + slot * kPairs : slot * C + kPairs;
 
   const int w = static_cast<int>(blockIdx.x) >= a.q_blocks;
   const unsigned block = w ? blockIdx.x - a.q_blocks : blockIdx.x;
@@ -229,22 +272,50 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
   const int groups = (heads + kGroup - 1) / kGroup;
   const unsigned n_items = static_cast<unsigned>(a.rows) * parts;
 
-  // this lane computes kOwn of its slot's four angles; lanes of the other heads the others
-  constexpr int kOwn = 4 / kHeads > 0 ? 4 / kHeads : 1;
+  // this lane computes kOwn of its slot's angles; lanes of the other heads the others
+  constexpr int kOwn = kPairs / kHeads > 0 ? kPairs / kHeads : 1;
   double turns[kOwn];
-  uint32_t axes = 0;
-  Pairs gain, acc;
+  uint64_t axes = 0;  // a byte a pair
+  Pairs<C> acc;
   bool have_lane = false;
   const float inv_hd = 1.0f / static_cast<float>(a.head_dim);
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) turns[i] = 0.0;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) acc.a[i] = acc.b[i] = 0ull;
+  for (int i = 0; i < C / 4; ++i) acc.a[i] = acc.b[i] = 0ull;
 
+  __shared__ uint4 s_turn[(MODE == kModeRope ? 4 : 6) * (C / 8) * kWarps * 32];
+  uint4* my_turn = s_turn + threadIdx.x;
+  // The ladder is a kernel argument, which lanes read one by one: once a block, not once a warp.
+  __shared__ double s_turns[128];
+  __shared__ __align__(8) uint8_t s_axis[128];
   const long long in_step = kHeads * in.head, out_step = kHeads * out.head;
-  for (unsigned item = block * kWarps + (threadIdx.x >> 5); item < n_items;
-       item += blocks * kWarps) {
-    unsigned row = item, b = 0;
+  long long grd_step = 0;
+  if constexpr (kBwd) grd_step = kHeads * a.grad[w].head;
+
+  // the item at hand: its token, its groups and the heads from this lane's first on
+  unsigned item = block * kWarps + (threadIdx.x >> 5), b = 0, t = 0;
+  int n_groups = 0, left = 0;
+  // this lane's channels of the next head to be loaded
+  const T* src = nullptr;
+  const T* grd = nullptr;
+  Raw<T, C> x[kPass], gy[kPass];
+  auto load = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) {
+      const bool on = live && i * kHeads < n;
+      x[i] = Raw<T, C>{};
+      if (on) load_raw<T, C, HALVES>(src, c0, c1, x[i]);
+      src += in_step;
+      if constexpr (kBwd) {
+        gy[i] = Raw<T, C>{};
+        if (on) load_raw<T, C, HALVES>(grd, c0, c1, gy[i]);
+        grd += grd_step;
+      }
+    }
+  };
+  auto open = [&]() {
+    unsigned row = item;
     int g0 = 0, g1 = groups;
     if (parts > 1) {
       row = item / parts;
@@ -252,81 +323,85 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
       g0 = groups * part / parts;
       g1 = groups * (part + 1) / parts;
     }
-    unsigned t = row;
+    t = row;
     if (a.rows != a.tokens) {
       b = row / static_cast<unsigned>(a.tokens);
       t = row - b * static_cast<unsigned>(a.tokens);
     }
-    // pointers to this lane's channels of the group's first head, stepped head by head
+    n_groups = g1 - g0;
     const int first = g0 * kGroup + sub;
-    const T* src = static_cast<const T*>(in.data) + b * in.batch + t * in.token + first * in.head;
-    T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token + first * out.head;
-    const T* grd = nullptr;
-    long long grd_step = 0;
-    if constexpr (kBwd) {
+    left = heads - first;
+    src = static_cast<const T*>(in.data) + b * in.batch + t * in.token + first * in.head;
+    if constexpr (kBwd)
       grd = static_cast<const T*>(a.grad[w].data) + b * a.grad[w].batch + t * a.grad[w].token +
             first * a.grad[w].head;
-      grd_step = kHeads * a.grad[w].head;
-    }
-    int left = heads - first;  // heads from this lane's on
-
-    Raw<T> x[kPass], gy[kPass];
-    auto load = [&](int n) {
-#pragma unroll
-      for (int i = 0; i < kPass; ++i) {
-        const bool on = live && i * kHeads < n;
-        x[i] = Raw<T>{};
-        if (on) load_raw<T, HALVES>(src, c0, c1, x[i]);
-        src += in_step;
-        if constexpr (kBwd) {
-          gy[i] = Raw<T>{};
-          if (on) load_raw<T, HALVES>(grd, c0, c1, gy[i]);
-          grd += grd_step;
-        }
-      }
-    };
     load(left);
+  };
+  bool more = item < n_items;
+  if (more) open();
+  if (a.n_pairs > 0) {
+    const int i = threadIdx.x;  // kWarps * 32 = 128 of them
+    s_turns[i] = i < a.n_pairs ? a.turns[i] : 0.0;
+    s_axis[i] = i < a.n_pairs ? a.axis[i] : uint8_t(0);
+    __syncthreads();
+  }
+  while (more) {
+    T* dst = static_cast<T*>(out.data) + b * out.batch + t * out.token + (heads - left) * out.head;
     if (!have_lane) {
       // this lane's constants, behind its first loads
       have_lane = true;
       if (turned) {
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) turns[i] = a.turns[slot * 4 + (sub * kOwn + i) % 4];
-        axes = *reinterpret_cast<const uint32_t*>(a.axis + slot * 4);
+        for (int i = 0; i < kOwn; ++i) turns[i] = s_turns[slot * kPairs + (sub * kOwn + i) % kPairs];
+        if constexpr (C == 16) axes = *reinterpret_cast<const uint64_t*>(s_axis + slot * kPairs);
+        else axes = *reinterpret_cast<const uint32_t*>(s_axis + slot * kPairs);
       }
       if constexpr (MODE != kModeRope) {
         const float* g = w ? a.k_gain : a.q_gain;
-        float ga[4], gb[4];
+        Pairs<C> gain;
+        float ga[kPairs], gb[kPairs];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kPairs; ++i) {
           const bool on = g != nullptr && live;
-          ga[i] = on ? __ldg(g + (HALVES && turned ? c0 + i : slot * 8 + member_a<HALVES>(i))) : 1.f;
-          gb[i] = on ? __ldg(g + (HALVES && turned ? c1 + i : slot * 8 + member_b<HALVES>(i))) : 1.f;
+          ga[i] = on ? __ldg(g + (HALVES && turned ? c0 + i : slot * C + member_a<C, HALVES>(i))) : 1.f;
+          gb[i] = on ? __ldg(g + (HALVES && turned ? c1 + i : slot * C + member_b<C, HALVES>(i))) : 1.f;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C / 4; ++i) {
           gain.a[i] = pack_f32x2(ga[2 * i], ga[2 * i + 1]);
           gain.b[i] = pack_f32x2(gb[2 * i], gb[2 * i + 1]);
         }
+        put<C>(my_turn, 4, gain.a);
+        put<C>(my_turn, 5, gain.b);
       }
     }
-    Turn turn;
     {
-      float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+      Turn<C> turn;
+      Pairs<C> gain;
+      if constexpr (MODE == kModeNorm) {
+        get<C>(my_turn, 4, gain.a);
+        get<C>(my_turn, 5, gain.b);
+      }
+      float cs[kPairs], sn[kPairs];
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        cs[i] = 1.f;
+        sn[i] = 0.f;
+      }
       if (a.n_pairs > 0) {
         const float* pos = a.pos + b * a.pos_batch + static_cast<size_t>(t) * a.n_axes;
         float oc[kOwn], os[kOwn];
 #pragma unroll
         for (int i = 0; i < kOwn; ++i) {
           // (a pair past the rotated width has turns 0: it stays)
-          const int p = (sub * kOwn + i) % 4;
-          sincos_turns(static_cast<double>(__ldg(pos + ((axes >> (8 * p)) & 0xffu))) * turns[i], os[i],
+          const int p = (sub * kOwn + i) % kPairs;
+          sincos_turns(static_cast<double>(__ldg(pos + static_cast<int>((axes >> (8 * p)) & 0xffu))) * turns[i], os[i],
                        oc[i]);
           if (kBwd || (MODE == kModeRope && a.inverse)) os[i] = -os[i];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (kOwn == 4) {
+        for (int i = 0; i < kPairs; ++i) {
+          if constexpr (kOwn == kPairs) {
             cs[i] = oc[i];
             sn[i] = os[i];
           } else {
@@ -336,7 +411,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < C / 4; ++i) {
         const uint64_t c = pack_f32x2(cs[2 * i], cs[2 * i + 1]), s = pack_f32x2(sn[2 * i], sn[2 * i + 1]);
         const uint64_t n = pack_f32x2(-sn[2 * i], -sn[2 * i + 1]);
         const bool folded = MODE == kModeNorm;  // y = rstd R(g x): the gains go into the turn
@@ -345,62 +420,78 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
         turn.as[i] = folded ? mul_f32x2(gain.a[i], s) : s;
         turn.bc[i] = folded ? mul_f32x2(gain.b[i], c) : c;
       }
+      put<C>(my_turn, 0, turn.ac);
+      put<C>(my_turn, 1, turn.nbs);
+      put<C>(my_turn, 2, turn.as);
+      put<C>(my_turn, 3, turn.bc);
     }
-    for (int g = g0; g < g1; ++g) {
-      Raw<T> xc[kPass], gc[kPass];
+    const int groups_here = n_groups;
+    int left_here = left;
+    for (int g = 0; g < groups_here; ++g) {
+      Raw<T, C> xc[kPass], gc[kPass];
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
         xc[i] = x[i];
         if constexpr (kBwd) gc[i] = gy[i];
       }
-      if (g + 1 < g1) load(left - kGroup);
+      // the next group's loads, or the next item's first
+      if (g + 1 < groups_here) {
+        load(left_here - kGroup);
+      } else {
+        item += blocks * kWarps;
+        more = item < n_items;
+        if (more) open();
+      }
 #pragma unroll
       for (int i = 0; i < kPass; ++i) {
-        Pairs f = widen<T, HALVES>(xc[i]);
+        Pairs<C> f = widen<T, C, HALVES>(xc[i]);
         if constexpr (MODE != kModeRope) {
-          const float rstd = rsqrtf(head_sum<LPH>(dot8(f, f)) * inv_hd + a.eps);
+          const float rstd = rsqrtf(head_sum<LPH>(dot(f, f)) * inv_hd + a.eps);
           const uint64_t r2 = pack_f32x2(rstd, rstd);
           if constexpr (!kBwd) {
             f = mul(f, r2);
           } else {
-            Pairs z = rotate(widen<T, HALVES>(gc[i]), turn);
+            Pairs<C> gain;
+            get<C>(my_turn, 4, gain.a);
+            get<C>(my_turn, 5, gain.b);
+            Pairs<C> z = rotate(widen<T, C, HALVES>(gc[i]), load_turn<C>(my_turn));
             f = mul(f, r2);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < C / 4; ++k) {
               acc.a[k] = fma_f32x2(z.a[k], f.a[k], acc.a[k]);
               acc.b[k] = fma_f32x2(z.b[k], f.b[k], acc.b[k]);
               z.a[k] = mul_f32x2(z.a[k], gain.a[k]);
               z.b[k] = mul_f32x2(z.b[k], gain.b[k]);
             }
-            const float dot = -head_sum<LPH>(dot8(z, f)) * inv_hd;
-            const uint64_t d2 = pack_f32x2(dot, dot);
+            const float zn = -head_sum<LPH>(dot(z, f)) * inv_hd;
+            const uint64_t d2 = pack_f32x2(zn, zn);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < C / 4; ++k) {
               f.a[k] = fma_f32x2(f.a[k], d2, z.a[k]);
               f.b[k] = fma_f32x2(f.b[k], d2, z.b[k]);
             }
             f = mul(f, r2);
           }
         }
-        if constexpr (!kBwd) f = rotate(f, turn);
-        if (live && i * kHeads < left) store_raw<T, HALVES>(dst, c0, c1, narrow<T, HALVES>(f));
+        if constexpr (!kBwd) f = rotate(f, load_turn<C>(my_turn));
+        if (live && i * kHeads < left_here) store_raw<T, C, HALVES>(dst, c0, c1, narrow<T, C, HALVES>(f));
         dst += out_step;
       }
-      left -= kGroup;
+      left_here -= kGroup;
     }
   }
   if constexpr (kBwd) {
     // the block's share of the gain's gradient: lanes of the same slot, then its warps in
     // order, then one row [head_dim] of the workspace
-    __shared__ float red[kWarps][LPH * 8];
-    float va[4], vb[4];
+    __shared__ float red[kWarps][LPH * C];
+    float va[kPairs], vb[kPairs];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C / 4; ++i) {
       unpack_f32x2(acc.a[i], va[2 * i], va[2 * i + 1]);
       unpack_f32x2(acc.b[i], vb[2 * i], vb[2 * i + 1]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
 #pragma unroll
       for (int o = LPH; o < 32; o <<= 1) {
         va[i] += __shfl_xor_sync(0xffffffffu, va[i], o);
@@ -408,8 +499,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE)) k_head_rows(
       }
       if (sub == 0 && live) {
         float* r = red[threadIdx.x >> 5];
-        r[HALVES && turned ? c0 + i : slot * 8 + member_a<HALVES>(i)] = va[i];
-        r[HALVES && turned ? c1 + i : slot * 8 + member_b<HALVES>(i)] = vb[i];
+        r[HALVES && turned ? c0 + i : slot * C + member_a<C, HALVES>(i)] = va[i];
+        r[HALVES && turned ? c1 + i : slot * C + member_b<C, HALVES>(i)] = vb[i];
       }
     }
     __syncthreads();
@@ -447,20 +538,34 @@ __global__ void __launch_bounds__(1024) k_gain_reduce(const float* __restrict__ 
   if (lane == 0 && blockIdx.x * 32 + warp < head_dim) out[blockIdx.x * 32 + warp] = v;
 }
 
-template <typename T, bool HALVES, int LPH, int MODE>
+template <typename T, int C, bool HALVES, int LPH, int MODE>
 int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
-  constexpr int kGroup = pass_count<T, MODE>() * (32 / LPH);
+  constexpr int kGroup = pass_count<T, C, MODE>() * (32 / LPH);
   const int sms = std::min(ctx.num_sms, kMaxSkCtas);
-  const long long most = 1ll * blocks_per_sm(MODE) * sms;
-  // Tokens alone keep an SM busy from about 24 of its warps on; with fewer, a token's groups
-  // of heads are dealt to several warps, each of which computes the token's angles again.
+  const long long most = 1ll * blocks_per_sm(MODE, C) * sms;
+  // An item is a token's heads (of q, or of k).  Where tokens are too few to keep the SMs busy
+  // that way, it is `per` groups of them: the number for which the warps that fit would be done
+  // first, each going through its share of the items one after the other, every item computing
+  // its token's angles again.
+  int groups[2];
+  for (int w = 0; w < 2; ++w) {
+    groups[w] = (a.heads[w] + kGroup - 1) / kGroup;
+    a.parts[w] = 1;
+  }
+  if (a.rows < 16ll * sms) {
+    long long best = -1;
+    for (int per = 1; per <= std::max(groups[0], groups[1]); per = per < 8 ? per + 1 : 2 * per) {
+      const long long n = a.rows * ((groups[0] + per - 1) / per + (groups[1] + per - 1) / per);
+      const long long time = (n + most * kWarps - 1) / (most * kWarps) * (per + kItemCost);
+      if (best >= 0 && time >= best) continue;
+      best = time;
+      for (int w = 0; w < 2; ++w) a.parts[w] = std::max(1, (groups[w] + per - 1) / per);
+    }
+  }
   long long items[2], cost[2];
   for (int w = 0; w < 2; ++w) {
-    const int groups = (a.heads[w] + kGroup - 1) / kGroup;
-    const long long want = a.rows > 0 ? (24ll * sms + a.rows - 1) / a.rows : 1;
-    a.parts[w] = static_cast<int>(std::max<long long>(1, std::min<long long>(groups, want)));
-    items[w] = groups > 0 ? a.rows * a.parts[w] : 0;
-    cost[w] = items[w] * (kItemCost + groups / a.parts[w]);
+    items[w] = groups[w] > 0 ? a.rows * a.parts[w] : 0;
+    cost[w] = items[w] * kItemCost + (groups[w] > 0 ? a.rows * groups[w] : 0);
   }
   // q's share of the blocks is its share of the work
   long long blocks[2];
@@ -470,7 +575,7 @@ int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
   }
   a.q_blocks = static_cast<int>(blocks[0]);
   if (blocks[0] + blocks[1] > 0) {
-    k_head_rows<T, HALVES, LPH, MODE>
+    k_head_rows<T, C, HALVES, LPH, MODE>
         <<<static_cast<unsigned>(blocks[0] + blocks[1]), kWarps * 32, 0, stream>>>(a);
     if (int rc = check_launch("head rows")) return rc;
   }
@@ -481,23 +586,31 @@ int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
   return check_launch("gain reduce");
 }
 
-template <typename T, bool HALVES, int LPH>
+template <typename T, int C, bool HALVES, int LPH>
 int launch_mode(const DevCtx& ctx, int mode, HeadRows& a, cudaStream_t stream) {
-  if (mode == kModeRope) return launch<T, HALVES, LPH, kModeRope>(ctx, a, stream);
-  if (mode == kModeNorm) return launch<T, HALVES, LPH, kModeNorm>(ctx, a, stream);
-  return launch<T, HALVES, LPH, kModeNormBwd>(ctx, a, stream);
+  if constexpr (C == 8)
+    if (mode == kModeRope) return launch<T, C, HALVES, LPH, kModeRope>(ctx, a, stream);
+  if (mode == kModeNorm) return launch<T, C, HALVES, LPH, kModeNorm>(ctx, a, stream);
+  return launch<T, C, HALVES, LPH, kModeNormBwd>(ctx, a, stream);
+}
+
+template <typename T, int C, bool HALVES>
+int launch_width(const DevCtx& ctx, int mode, HeadRows& a, cudaStream_t stream) {
+  if (a.head_dim <= 64) return launch_mode<T, C, HALVES, 64 / C>(ctx, mode, a, stream);
+  if (a.head_dim <= 128) return launch_mode<T, C, HALVES, 128 / C>(ctx, mode, a, stream);
+  return launch_mode<T, C, HALVES, 256 / C>(ctx, mode, a, stream);
 }
 
 template <typename T>
 int launch_type(const DevCtx& ctx, int mode, HeadRows& a, bool halves, cudaStream_t stream) {
-  const int hd = a.head_dim;
-  if (halves)
-    return hd <= 64    ? launch_mode<T, true, 8>(ctx, mode, a, stream)
-           : hd <= 128 ? launch_mode<T, true, 16>(ctx, mode, a, stream)
-                       : launch_mode<T, true, 32>(ctx, mode, a, stream);
-  return hd <= 64    ? launch_mode<T, false, 8>(ctx, mode, a, stream)
-         : hd <= 128 ? launch_mode<T, false, 16>(ctx, mode, a, stream)
-                     : launch_mode<T, false, 32>(ctx, mode, a, stream);
+  // (the rotation alone has nothing to gain: 47 us against 51 at 2 x 11,344 tokens)
+  if constexpr (sizeof(T) == 2) {
+    if (mode != kModeRope && a.head_dim % 16 == 0 && (!halves || a.n_pairs % 8 == 0))
+      return halves ? launch_width<T, 16, true>(ctx, mode, a, stream)
+                    : launch_width<T, 16, false>(ctx, mode, a, stream);
+  }
+  return halves ? launch_width<T, 8, true>(ctx, mode, a, stream)
+                : launch_width<T, 8, false>(ctx, mode, a, stream);
 }
 
 }  // namespace

@@ -649,63 +649,72 @@ _DTYPES = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32
 
 
 def _lead(t, name: str):
-    """Shape, element type and device of a call's first tensor [(batch,) tokens, heads,
+    """Shape, element type and device index of a call's first tensor [(batch,) tokens, heads,
     head_dim], which the others have to agree with."""
     shape = t.shape
-    if not t.is_cuda or len(shape) not in (3, 4):
+    dev = t.get_device()
+    if dev < 0 or not 3 <= len(shape) <= 4:
         raise TypeError(f"{name}: expected a CUDA tensor [batch, tokens, heads, head_dim] or "
                         f"[tokens, heads, head_dim], got {t.device} {tuple(shape)}")
-    if t.get_device() != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current device")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name}: {t.dtype} is not bf16, fp16 or fp32")
-    return shape, t.dtype, t.device
+    return shape, t.dtype, dev
 
 
-def _heads(t, name: str, shape, dtype, device) -> HeadView:
-    if t.shape != shape or t.dtype is not dtype or t.device != device:
-        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on {device}, got "
-                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+def _heads(t, name: str, shape, dtype, dev: int) -> HeadView:
     s = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{dev}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
     if s[-1] != 1 and shape[-1] != 1:
         raise ValueError(f"{name}: head_dim must be contiguous")
-    return HeadView(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+    if len(s) == 4:
+        return HeadView(t.data_ptr(), s[0], s[1], s[2])
+    return HeadView(t.data_ptr(), 0, s[0], s[1])
 
 
-def _vector(t, name: str, n: int, device, dtype=torch.float32):
+def _vector(t, name: str, n: int, dev: int, dtype=torch.float32):
     """Data pointer of an optional contiguous vector of n elements."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on {device}, got "
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} values on cuda:{dev}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _positions(plan, pos, shape, device):
+def _positions(plan, pos, shape, dev: int):
     """(pointer, batch stride) of pos [tokens, axes] or [batch, tokens, axes] fp32."""
     if plan is None:
         return None, 0
     if pos is None:
         raise ValueError("pos: a plan needs positions")
-    ps = pos.shape
+    ps, axes = pos.shape, plan.n_axes
     one = len(ps) == 2
-    if ((ps[-2:] != (shape[-3], plan.n_axes) if len(ps) >= 2 else True)
-            or not (one or (len(ps) == 3 and len(shape) == 4 and ps[0] == shape[0]))
-            or pos.dtype is not torch.float32 or pos.device != device):
-        raise ValueError(f"pos: expected [tokens, {plan.n_axes}] or [batch, tokens, {plan.n_axes}] "
-                         f"fp32 on {device} for {tuple(shape)}, got {tuple(ps)} {pos.dtype} on "
-                         f"{pos.device}")
+    if (not (one or (len(ps) == 3 and len(shape) == 4 and ps[0] == shape[0])) or ps[-1] != axes
+            or ps[-2] != shape[-3] or pos.dtype is not torch.float32 or pos.get_device() != dev):
+        raise ValueError(f"pos: expected [tokens, {axes}] or [batch, tokens, {axes}] fp32 on "
+                         f"cuda:{dev} for {tuple(shape)}, got {tuple(ps)} {pos.dtype} on {pos.device}")
     s = pos.stride()
-    if (s[-1] != 1 and ps[-1] > 1) or (s[-2] != ps[-1] and ps[-2] > 1):
+    if (s[-1] != 1 and axes > 1) or (s[-2] != axes and ps[-2] > 1):
         raise ValueError("pos: the positions of a sequence must be contiguous")
     return pos.data_ptr(), 0 if one else s[0]
 
 
-def _raw_stream(stream, device):
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(device.index)
+def _scratch(ws, dev: int):
+    """(pointer, bytes) of a workspace on the call's device."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous buffer on cuda:{dev}, got one on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _raw_stream(stream, dev: int):
+    # (the current stream's handle without the Stream object that _stream makes)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def make_rope_axes(split: Sequence[int], theta: float = 10000.0, pairing: int = ROPE_ADJACENT,
@@ -723,12 +732,12 @@ def rope_axes(plan: RopePlan, x, pos, out, inverse: bool = False, stream=None) -
     """out = x [(batch,) tokens, heads, head_dim] (bf16, fp16 or fp32; any strides with
     head_dim contiguous) rotated at pos [(batch,) tokens, axes] fp32.  inverse: turned back,
     which is the gradient of the rotation.  out may be x."""
-    shape, dtype, device = _lead(x, "x")
-    pp, ps = _positions(plan, pos, shape, device)
-    _check(lib.h3b_rope_axes(plan, _DTYPES[dtype], _heads(x, "x", shape, dtype, device),
+    shape, dtype, dev = _lead(x, "x")
+    pp, ps = _positions(plan, pos, shape, dev)
+    _check(lib.h3b_rope_axes(plan, _DTYPES[dtype], _heads(x, "x", shape, dtype, dev),
                              shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], shape[-1],
-                             pp, ps, 1 if inverse else 0, _heads(out, "out", shape, dtype, device),
-                             _raw_stream(stream, device)))
+                             pp, ps, 1 if inverse else 0, _heads(out, "out", shape, dtype, dev),
+                             _raw_stream(stream, dev)))
 
 
 def _k_shape(shape, k):
@@ -742,18 +751,18 @@ def qk_norm_rope(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos
                  stream=None) -> None:
     """RMS norm of every head of q and k (gains [head_dim] fp32 or None), then the rotation
     of rope_axes (plan None: none).  k may have fewer heads than q, or be None."""
-    shape, dtype, device = _lead(q, "q")
+    shape, dtype, dev = _lead(q, "q")
     hd = shape[-1]
-    pp, ps = _positions(plan, pos, shape, device)
+    pp, ps = _positions(plan, pos, shape, dev)
     ks, kv_heads = _k_shape(shape, k)
     _check(lib.h3b_qk_norm_rope(
-        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, device),
-        None if k is None else _heads(k, "k", ks, dtype, device),
+        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, dev),
+        None if k is None else _heads(k, "k", ks, dtype, dev),
         shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], kv_heads, hd,
-        _vector(q_gain, "q_gain", hd, device), _vector(k_gain, "k_gain", hd, device), eps, pp, ps,
-        _heads(q_out, "q_out", shape, dtype, device),
-        None if k is None else _heads(k_out, "k_out", ks, dtype, device),
-        _raw_stream(stream, device)))
+        _vector(q_gain, "q_gain", hd, dev), _vector(k_gain, "k_gain", hd, dev), eps, pp, ps,
+        _heads(q_out, "q_out", shape, dtype, dev),
+        None if k is None else _heads(k_out, "k_out", ks, dtype, dev),
+        _raw_stream(stream, dev)))
 
 
 def qk_norm_rope_backward_workspace_size(head_dim: int) -> int:
@@ -767,23 +776,23 @@ def qk_norm_rope_backward(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: f
                           g_k, dq, dk, dq_gain, dk_gain, ws, stream=None) -> None:
     """Gradients of qk_norm_rope: from its inputs and the gradients g_q, g_k of its outputs to
     dq, dk (may be g_q, g_k) and dq_gain, dk_gain [head_dim] fp32 (None: not wanted)."""
-    shape, dtype, device = _lead(q, "q")
+    shape, dtype, dev = _lead(q, "q")
     hd = shape[-1]
-    pp, ps = _positions(plan, pos, shape, device)
+    pp, ps = _positions(plan, pos, shape, dev)
     ks, kv_heads = _k_shape(shape, k)
-    wp, wb = _wsargs(ws)
+    wp, wb = _scratch(ws, dev)
 
     def kview(t, name):
-        return None if k is None else _heads(t, name, ks, dtype, device)
+        return None if k is None else _heads(t, name, ks, dtype, dev)
 
     _check(lib.h3b_qk_norm_rope_backward(
-        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, device), kview(k, "k"),
+        plan, _DTYPES[dtype], _heads(q, "q", shape, dtype, dev), kview(k, "k"),
         shape[0] if len(shape) == 4 else 1, shape[-3], shape[-2], kv_heads, hd,
-        _vector(q_gain, "q_gain", hd, device), _vector(k_gain, "k_gain", hd, device), eps, pp, ps,
-        _heads(g_q, "g_q", shape, dtype, device), kview(g_k, "g_k"),
-        _heads(dq, "dq", shape, dtype, device), kview(dk, "dk"),
-        _vector(dq_gain, "dq_gain", hd, device), _vector(dk_gain, "dk_gain", hd, device), wp, wb,
-        _raw_stream(stream, device)))
+        _vector(q_gain, "q_gain", hd, dev), _vector(k_gain, "k_gain", hd, dev), eps, pp, ps,
+        _heads(g_q, "g_q", shape, dtype, dev), kview(g_k, "g_k"),
+        _heads(dq, "dq", shape, dtype, dev), kview(dk, "dk"),
+        _vector(dq_gain, "dq_gain", hd, dev), _vector(dk_gain, "dk_gain", hd, dev), wp, wb,
+        _raw_stream(stream, dev)))
 
 
 def attention_prefix_workspace_size(batch: int, n_q: int, n_heads: int, n_kv_heads: int,
@@ -803,7 +812,7 @@ def attention_prefix(q, k_prefix, v_prefix, k, v, out, kv_len=None, q_len=None,
     the queries are the last q_len[b] tokens of their sequence.  Rows from q_len[b] (None:
     n_q) on are left as they were.  scale 0: 1 / sqrt(head_dim).  ws: a device buffer of
     attention_prefix_workspace_size bytes."""
-    shape, dtype, device = _lead(q, "q")
+    shape, dtype, dev = _lead(q, "q")
     if len(shape) != 4:
         raise TypeError(f"q: expected [batch, n_q, heads, head_dim], got {tuple(shape)}")
     batch, n_q, heads, hd = shape
@@ -812,20 +821,20 @@ def attention_prefix(q, k_prefix, v_prefix, k, v, out, kv_len=None, q_len=None,
     if k_prefix is not None:
         n_prefix, kv_heads = k_prefix.shape[0], k_prefix.shape[-2]
         ps = (n_prefix, kv_heads, hd)
-        vkp = _heads(k_prefix, "k_prefix", ps, dtype, device)
-        vvp = _heads(v_prefix, "v_prefix", ps, dtype, device)
+        vkp = _heads(k_prefix, "k_prefix", ps, dtype, dev)
+        vvp = _heads(v_prefix, "v_prefix", ps, dtype, dev)
     if k is not None:
         n_kv = k.shape[1]
         kv_heads = kv_heads or k.shape[-2]
         ks = (batch, n_kv, kv_heads, hd)
-        vk = _heads(k, "k", ks, dtype, device)
-        vv = _heads(v, "v", ks, dtype, device)
-    wp, wb = _wsargs(ws)
+        vk = _heads(k, "k", ks, dtype, dev)
+        vv = _heads(v, "v", ks, dtype, dev)
+    wp, wb = _scratch(ws, dev)
     _check(lib.h3b_attention_prefix(
-        _DTYPES[dtype], _heads(q, "q", shape, dtype, device), vkp, vvp, vk, vv, batch, n_q, heads,
-        kv_heads, hd, n_prefix, n_kv, _vector(kv_len, "kv_len", batch, device, torch.int32),
-        _vector(q_len, "q_len", batch, device, torch.int32), 1 if causal else 0, scale,
-        _heads(out, "out", shape, dtype, device), wp, wb, _raw_stream(stream, device)))
+        _DTYPES[dtype], _heads(q, "q", shape, dtype, dev), vkp, vvp, vk, vv, batch, n_q, heads,
+        kv_heads, hd, n_prefix, n_kv, _vector(kv_len, "kv_len", batch, dev, torch.int32),
+        _vector(q_len, "q_len", batch, dev, torch.int32), 1 if causal else 0, scale,
+        _heads(out, "out", shape, dtype, dev), wp, wb, _raw_stream(stream, dev)))
 
 
 def layer_mask(mods_host: np.ndarray, n_active: int) -> np.ndarray:
