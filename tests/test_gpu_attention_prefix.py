@@ -137,6 +137,20 @@ def test_ragged_lengths(size, causal):
     check(call(*t, **kw), *t, **kw)
 
 
+@pytest.mark.parametrize("size", [(1100, 1, 4, 2, 64, 200, 40), (2500, 1, 2, 2, 64, 0, 140),
+                                  (700, 5, 2, 1, 128, 130, 9)], ids=str)
+def test_many_sequences(size):
+    """More sequences than lanes and than blocks; whole stretches of them empty."""
+    g = np.random.default_rng(11)
+    kv_len = g.integers(0, size[6] + 1, size[0]).tolist()
+    kv_len[40:90] = [0] * 50
+    q_len = g.integers(0, size[1] + 1, size[0]).tolist()
+    q_len[64:128] = [0] * 64
+    d = make(*size, BF, seed=12, kv_len=kv_len, q_len=q_len)
+    lens = dict(kv_len=kv_len, q_len=q_len)
+    check(call(*d, **lens, causal=True), *d, **lens, causal=True)
+
+
 def test_lengths_are_clamped():
     t = make(3, 5, 2, 1, 64, 40, 30, BF)
     kw = dict(kv_len=[99, -5, 30], q_len=[5, 1000, -1], causal=False)

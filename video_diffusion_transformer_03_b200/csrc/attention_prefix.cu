@@ -698,6 +698,11 @@ __device__ __forceinline__ int lane_scan(int v, int lane) {
   return v;
 }
 
+// Work of a sequence's own units; 0 behind the batch.
+__device__ __forceinline__ int narrow_own_work(const PrefixArgs& a, int b) {
+  return b < a.batch ? a.own_units * narrow_work(narrow_steps(lens_of(a, b))) : 0;
+}
+
 // The CTA's first segment.  All lanes of a warp.
 __device__ inline NarrowWalk narrow_first(const PrefixArgs& a, int lane, int cta) {
   const int far = narrow_prefix_work(a);
@@ -1122,122 +1127,120 @@ __device__ __forceinline__ Side narrow_side(const PrefixArgs& a, const Cut& all,
 }
 
 // Joins the states of a row of the output: WARPS warps per (sequence, query, head), each with
-// its share of the states, lanes over the channels.  Launched while k_prefix_narrow runs: the
-// schedule is worked out before the wait for it, only the states' two loads come after.
+// its share of the channels, lanes over those and over the states.  Launched while k_prefix_narrow runs: the
+// first rows' schedule is worked out before the wait for it, only the states' two loads come
+// after.  A block takes 4 / WARPS rows at a time of a range of rows, which is that many where
+// rows are few; where they are many it is longer, so that the whole batch's lengths are not
+// summed for every row.
 template <typename T, int HD, int WARPS>
-__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixArgs a) {
-  constexpr int kPer = HD / 32;
-  constexpr int kRows = 4 / WARPS;  // rows of a block
-  __shared__ int s_start[kRows], s_total;
-  __shared__ float s_part[WARPS > 1 ? 4 : 1][HD + 2];
+__global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ PrefixArgs a, int per) {
+  constexpr int kRows = 4 / WARPS;              // rows of a block at a time
+  constexpr int kLanes = HD / (4 * WARPS);      // lanes that have a state's channels, 4 each
+  constexpr int kStates = 32 / kLanes;          // states at a time
+  __shared__ int s_sum[2][4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int in_block = warp / WARPS, sub = warp % WARPS;
-  const int row = blockIdx.x * kRows + in_block;
-  const int b = row / (a.n_q * a.heads), in_b = row - b * a.n_q * a.heads;
-  const int tok = in_b / a.heads, h = in_b - tok * a.heads;
-  if (warp == 0) {
-    // where the rows' sequences' own work starts
-    int base = narrow_prefix_work(a);
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int own =
-          b0 + lane < a.batch ? a.own_units * narrow_work(narrow_steps(lens_of(a, b0 + lane))) : 0;
-      const int end = lane_scan(own, lane);
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if ((blockIdx.x * kRows + r) / (a.n_q * a.heads) == b0 + lane) s_start[r] = base + end - own;
-      base += __shfl_sync(0xffffffffu, end, 31);
-    }
-    if (lane == 0) s_total = base;
-  }
-  __syncthreads();
-  const int total = s_total;
-  Lens len{0, 0};
-  if (b < a.batch) len = lens_of(a, b);
-  const bool on = b < a.batch && tok < len.q;
-  Side side[2];
-  side[0].n = side[1].n = 0;
-  if (on && total > 0) {
-    const Cut all = cut(total, narrow_ctas(total, a.ctas));
-    const int kvh = h / a.group, hg = (h - kvh * a.group) / a.gt;
-    const int g = h - kvh * a.group - hg * a.gt, hh = kvh * a.head_groups + hg;
-    if (a.prefix_units > 0) {
-      const int chunk = b / a.bt, index = hh * a.chunks + chunk;
-      side[0] = narrow_side(a, all, true, index, index * narrow_work(a.prefix_tiles), a.prefix_tiles,
-                            ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok);
-    }
-    const int steps = narrow_steps(len);
-    if (steps > 0)
-      side[1] = narrow_side(a, all, false, a.prefix_units + b * a.own_units + hh,
-                            s_start[in_block] + hh * narrow_work(steps), steps, g * a.n_q + tok);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (max, sum) of the first 32 states of each side, a lane each; more are read again
-  auto state = [&](const Side& s, int i) -> float2 {
-    if (i >= s.n) return make_float2(-INFINITY, 0.f);
-    return __ldcg(a.part_sums + s.row + (i >> 1) * s.step + (i & 1) * s.chain);
-  };
-  float2 ml[2];
-#pragma unroll
-  for (int d = 0; d < 2; ++d) ml[d] = state(side[d], lane);
-  float top = fmaxf(ml[0].x, ml[1].x);
-#pragma unroll
-  for (int d = 0; d < 2; ++d)
-    for (int i = lane + 32; i < side[d].n; i += 32) top = fmaxf(top, state(side[d], i).x);
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  float l = 0.f, o[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-#pragma unroll
-  for (int d = 0; d < 2; ++d) {
-    for (int i0 = 0; i0 < side[d].n; i0 += 32) {
-      const float2 one = i0 == 0 ? ml[d] : state(side[d], i0 + lane);
-      const float wt = weight_of(one.x, top);
-      l = fmaf(one.y, wt, l);
-      const int n = min(32, side[d].n - i0);
+  const int far = narrow_prefix_work(a);
+  const int per_b = a.n_q * a.heads, rows = a.batch * per_b;
+  const int times = (rows + kRows - 1) / kRows;
+  const int time0 = blockIdx.x * per, time1 = min(times, time0 + per);
+  const int mine = lane / kLanes;                                    // states mine, mine + kStates ..
+  const int chan = (sub * kLanes + lane % kLanes) * 4;
+  // the work in front of the block's first sequence, and all of it
+  int at_b = time0 * kRows / per_b, at_base, total;
+  {
+    int before = 0, sum = 0;
 #pragma unroll 4
-      for (int i = sub; i < n; i += WARPS) {
-        const float w = __shfl_sync(0xffffffffu, wt, i);
-        if (w == 0.f) continue;  // a chain without steps, or a state that no longer counts
-        const float* src = a.part_rows +
-                           (side[d].row + ((i0 + i) >> 1) * side[d].step + (i & 1) * side[d].chain) * HD +
-                           lane * kPer;
-        if constexpr (kPer == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+    for (int b = threadIdx.x; b < a.batch; b += 128) {
+      const int own = narrow_own_work(a, b);
+      sum += own;
+      if (b < at_b) before += own;
+    }
+    before = __reduce_add_sync(0xffffffffu, before);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    if (lane == 0) {
+      s_sum[0][warp] = before;
+      s_sum[1][warp] = sum;
+    }
+    __syncthreads();
+    at_base = far + s_sum[0][0] + s_sum[0][1] + s_sum[0][2] + s_sum[0][3];
+    total = far + s_sum[1][0] + s_sum[1][1] + s_sum[1][2] + s_sum[1][3];
+  }
+  for (int time = time0; time < time1; ++time) {
+    const int row = time * kRows + in_block;
+    const int b = row / per_b, in_b = row - b * per_b;
+    const int tok = in_b / a.heads, h = in_b - tok * a.heads;
+    while (at_b < b) at_base += narrow_own_work(a, at_b++);
+    Lens len{0, 0};
+    if (b < a.batch) len = lens_of(a, b);
+    const bool on = b < a.batch && tok < len.q;
+    Side side[2];
+    side[0].n = side[1].n = 0;
+    if (on && total > 0) {
+      const Cut all = cut(total, narrow_ctas(total, a.ctas));
+      const int kvh = h / a.group, hg = (h - kvh * a.group) / a.gt;
+      const int g = h - kvh * a.group - hg * a.gt, hh = kvh * a.head_groups + hg;
+      if (a.prefix_units > 0) {
+        const int chunk = b / a.bt, index = hh * a.chunks + chunk;
+        side[0] = narrow_side(a, all, true, index, index * narrow_work(a.prefix_tiles), a.prefix_tiles,
+                              ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok);
+      }
+      const int steps = narrow_steps(len);
+      if (steps > 0)
+        side[1] = narrow_side(a, all, false, a.prefix_units + b * a.own_units + hh,
+                              at_base + hh * narrow_work(steps), steps, g * a.n_q + tok);
+    }
+    if (time == time0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (max, sum) of the first 32 states of each side, a lane each; more are read again
+    auto state = [&](const Side& s, int i) -> float2 {
+      if (i >= s.n) return make_float2(-INFINITY, 0.f);
+      return __ldcg(a.part_sums + s.row + (i >> 1) * s.step + (i & 1) * s.chain);
+    };
+    float2 ml[2];
+#pragma unroll
+    for (int d = 0; d < 2; ++d) ml[d] = state(side[d], lane);
+    float top = fmaxf(ml[0].x, ml[1].x);
+#pragma unroll
+    for (int d = 0; d < 2; ++d)
+      for (int i = lane + 32; i < side[d].n; i += 32) top = fmaxf(top, state(side[d], i).x);
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int d = 0; d < 2; ++d) {
+      for (int i0 = 0; i0 < side[d].n; i0 += 32) {
+        const float2 one = i0 == 0 ? ml[d] : state(side[d], i0 + lane);
+        const float wt = weight_of(one.x, top);
+        l = fmaf(one.y, wt, l);
+        const int n = min(32, side[d].n - i0);
+#pragma unroll 4
+        for (int i1 = 0; i1 < n; i1 += kStates) {
+          const int i = i1 + mine;
+          const float w = __shfl_sync(0xffffffffu, wt, i & 31);
+          // 0: a chain without steps, or a state that no longer counts
+          if (i >= n || w == 0.f) continue;
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(
+              a.part_rows +
+              (side[d].row + ((i0 + i) >> 1) * side[d].step + (i & 1) * side[d].chain) * HD + chan));
           o[0] = fmaf(v.x, w, o[0]);
           o[1] = fmaf(v.y, w, o[1]);
           o[2] = fmaf(v.z, w, o[2]);
           o[3] = fmaf(v.w, w, o[3]);
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          o[0] = fmaf(v.x, w, o[0]);
-          o[1] = fmaf(v.y, w, o[1]);
         }
       }
     }
-  }
 #pragma unroll
-  for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
-  if constexpr (WARPS > 1) {
-    // the warps' shares, added in order
+    for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) s_part[warp][lane * kPer + e] = o[e];
-    __syncthreads();
-    if (sub != 0) return;
+    for (int s = 16; s >= kLanes; s >>= 1)
 #pragma unroll
-    for (int v = 1; v < WARPS; ++v)
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] += s_part[warp + v][lane * kPer + e];
-  }
-  if (!on) return;
-  const float inv_l = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-  T* dst = static_cast<T*>(a.out.data) + b * a.out.batch + tok * a.out.token + h * a.out.head +
-           lane * kPer;
-  if constexpr (kPer == 4)
+      for (int e = 0; e < 4; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], s);
+    if (!on || mine != 0) continue;
+    const float inv_l = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    T* dst = static_cast<T*>(a.out.data) + b * a.out.batch + tok * a.out.token + h * a.out.head + chan;
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(o[0] * inv_l, o[1] * inv_l),
                                                 pack2<T>(o[2] * inv_l, o[3] * inv_l));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack2<T>(o[0] * inv_l, o[1] * inv_l);
+  }
 }
 
 // A [batch, tokens, heads, HD] view as a TMA map whose box is 64 channels of box_tokens tokens
@@ -1301,6 +1304,9 @@ int launch_wide(const DevCtx& ctx, PrefixArgs a, cudaStream_t stream) {
   return check_launch("attention_prefix");
 }
 
+// Blocks of the join an SM gets at most.
+constexpr long long kJoinBlocks = 16;
+
 template <typename T, int HD>
 int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
   using Cfg = NarrowCfg<HD>;
@@ -1321,7 +1327,9 @@ int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
   const long long rows = 1ll * a.batch * a.n_q * a.heads;
   const bool many = a.prefix_units > 0 && 2 * a.ctas >= 8 * a.prefix_units;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(many ? rows : (rows + 3) / 4));
+  const long long times = many ? rows : (rows + 3) / 4;
+  const int per = static_cast<int>((times + kJoinBlocks * a.ctas - 1) / (kJoinBlocks * a.ctas));
+  cfg.gridDim = dim3(static_cast<unsigned>((times + per - 1) / per));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr = {};
@@ -1329,8 +1337,8 @@ int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (many) cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 4>, a);
-  else cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 1>, a);
+  if (many) cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 4>, a, per);
+  else cudaLaunchKernelEx(&cfg, k_prefix_join<T, HD, 1>, a, per);
   return check_launch("attention_prefix join");
 }
 

@@ -160,7 +160,7 @@ inline long long wide_work_cap(const PrefixArgs& a) {
 // every sequence's own, (sequence, key head, group of query heads).  A unit's rows are its
 // sequences' queries of those heads; its steps the 128-key tiles of the prefix or of the
 // sequence.  Units without keys or queries have no work.
-constexpr int kNarrowStep = 4, kNarrowUnit = 8;  // cost of a step; of a unit's start and end
+constexpr int kNarrowStep = 4, kNarrowUnit = 6;  // cost of a step; of a unit's start and end
 
 struct NarrowUnit {
   int index;        // prefix units, then batch x own units
