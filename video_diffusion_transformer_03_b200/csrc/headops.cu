@@ -255,6 +255,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_ro
   constexpr int kHeads = 32 / LPH;
   constexpr int kGroup = kPass * kHeads;
   constexpr bool kBwd = MODE == kModeNormBwd;
+  // (the backward pass's second kernel may be launched; it waits for this one's end)
+  if constexpr (kBwd) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int slot = lane % LPH, sub = lane / LPH;
   constexpr int kPairs = C / 2;
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_ro
 
 // Gains' gradients from the blocks' rows, in a fixed order: a block per 32 columns of one
 // gain (blockIdx.y: q or k), warp j takes rows j, j + 32, ..., then the 32 sums are added.
-__global__ void __launch_bounds__(1024) k_gain_reduce(const float* __restrict__ part, int q_rows,
+__global__ void __launch_bounds__(1024) k_gain_reduce(const float* part, int q_rows,
                                                       int k_rows, int head_dim,
                                                       float* __restrict__ dq_gain,
                                                       float* __restrict__ dk_gain) {
@@ -526,6 +528,7 @@ __global__ void __launch_bounds__(1024) k_gain_reduce(const float* __restrict__ 
   if (blockIdx.y) part += static_cast<size_t>(q_rows) * head_dim;
   float* out = blockIdx.y ? dk_gain : dq_gain;
   if (out == nullptr) return;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float v = 0.f;
   if (col < head_dim)
 #pragma unroll 4
@@ -580,9 +583,18 @@ int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
     if (int rc = check_launch("head rows")) return rc;
   }
   if (MODE != kModeNormBwd || (!a.dq_gain && !a.dk_gain)) return 0;
-  k_gain_reduce<<<dim3((a.head_dim + 31) / 32, 2), 1024, 0, stream>>>(
-      a.part, static_cast<int>(blocks[0]), static_cast<int>(blocks[1]), a.head_dim, a.dq_gain,
-      a.dk_gain);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.head_dim + 31) / 32, 2);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, k_gain_reduce, static_cast<const float*>(a.part),
+                     static_cast<int>(blocks[0]), static_cast<int>(blocks[1]), a.head_dim, a.dq_gain,
+                     a.dk_gain);
   return check_launch("gain reduce");
 }
 
