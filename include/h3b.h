@@ -620,7 +620,7 @@ int h3b_rope_axes(const h3b_rope_plan* plan, int dtype, const h3b_head_view* x, 
                   void* stream);
 
 /* Per-head RMS norm of q and k with the rotation in the same pass:
- *   y = R(x / sqrt(mean(x^2) + eps) * gain)          per token and head.
+ *   y = R(x / sqrt(mean(x^2) + eps) * gain)          per token and head, the squares in fp32.
  * q, q_out [batch, n_tokens, n_q_heads, head_dim], k, k_out with n_k_heads (0: no k, its
  * arguments are ignored); gains [head_dim] fp32 (device; NULL = ones).  plan == NULL: no
  * rotation (pos is ignored).  Sizes, positions, rounding and in-place use as h3b_rope_axes. */
@@ -667,7 +667,9 @@ int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_he
  * Scores, softmax and sums are fp32; the weights are rounded to the type for the product with
  * the values.  Equal calls give equal bits.
  * ws: device scratch, 16-byte aligned, of h3b_attention_prefix_workspace_size bytes; one call
- * at a time per buffer, nothing in it has to be zero.  out must not overlap the inputs. */
+ * at a time per buffer, nothing in it has to be zero.  out must not overlap the inputs.
+ * A call of more than some 10^8 tiles of 256 queries and 128 keys is refused (H3B_EINVAL, a
+ * workspace size of 0); batch <= 65535. */
 size_t h3b_attention_prefix_workspace_size(int batch, int n_q, int n_heads, int n_kv_heads,
                                            int head_dim, int n_prefix, int n_kv);
 int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view* k_prefix,

@@ -108,6 +108,8 @@ SIZES = [
     (1, 16, 16, 2, 64, 63, 17), (4, 33, 6, 3, 128, 129, 40), (1, 128, 2, 1, 128, 128, 128),
     (2, 129, 3, 3, 64, 100, 129), (1, 300, 2, 1, 128, 513, 300), (2, 515, 4, 2, 64, 0, 515),
     (1, 1600, 3, 3, 128, 1024, 1600), (70, 2, 3, 3, 64, 20, 9),
+    # a key head's query heads in uneven groups
+    (3, 48, 6, 2, 64, 140, 130), (2, 20, 7, 1, 128, 129, 70),
     # keys and values past the L2: their tiles arrive in any order
     (40, 1, 12, 12, 128, 6000, 1100),
 ]
@@ -372,6 +374,11 @@ def test_binding_refuses():
             h3b.attention_prefix(*bad, ws=ws)
     with pytest.raises(TypeError):
         h3b.attention_prefix(q[0], kp, vp, k, v, out[0], ws=ws)
+    for bad in ((q, kp, None, k, v, out), (q, kp, vp, k, None, out), (q, kp, vp, k, v, None)):
+        with pytest.raises(TypeError):
+            h3b.attention_prefix(*bad, ws=ws)
+    with pytest.raises(ValueError):
+        h3b.attention_prefix(q, kp, vp, k, v, out, ws=ws.cpu())
     for kw in (dict(kv_len=torch.zeros(2, dtype=torch.int64, device=DEV)),
                dict(kv_len=torch.zeros(3, dtype=torch.int32, device=DEV)),
                dict(q_len=torch.zeros(2, dtype=torch.int32))):

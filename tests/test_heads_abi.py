@@ -114,6 +114,9 @@ def rope(plan="ok", dtype=0, x=None, batch=2, tokens=16, heads=4, hd=128, pos=P,
 def test_rope_axes_refusals():
     refused(rope(plan=None), "plan is NULL")
     refused(rope(plan=h3b.RopePlan()), "not made by")
+    odd = h3b.make_rope_axes((16, 16), pairing=h3b.ROPE_HALVES)
+    odd.n_pairs = 6
+    refused(rope(plan=odd), "not made by")
     refused(rope(dtype=3), "dtype")
     refused(rope(batch=-1), "sizes")
     refused(rope(tokens=-1), "sizes")
@@ -197,3 +200,14 @@ def test_attention_prefix_refusals():
         assert attend(ws=ws, nbytes=nbytes) == h3b.H3B_EWORKSPACE
     with pytest.raises(h3b.H3BError, match="n_heads"):
         h3b.attention_prefix_workspace_size(2, 3, 4, 3, 64, 16, 8)
+
+
+def test_attention_prefix_refuses_more_work_than_it_counts():
+    # 10^9 tiles: the size query and the call say so
+    assert h3b.lib.h3b_attention_prefix_workspace_size(1000, 4096, 64, 64, 64, 1 << 25, 0) == 0
+    assert "too much work" in h3b.lib.h3b_last_error().decode()
+    with pytest.raises(h3b.H3BError, match="too much work"):
+        h3b.attention_prefix_workspace_size(60000, 1, 64, 1, 128, 1 << 28, 1 << 20)
+    with pytest.raises(h3b.H3BError, match="too much work"):
+        h3b.attention_prefix_workspace_size(65535, 1 << 24, 65536, 65536, 64, 1 << 28, 1 << 28)
+    assert h3b.attention_prefix_workspace_size(60000, 1, 64, 1, 128, 1000, 1000) > 0

@@ -215,7 +215,8 @@ int head_rows_common(const char* who, const h3b_rope_plan* plan, int dtype, int 
   a->head_dim = head_dim;
   if (!plan) return H3B_OK;
   if (plan->magic != kRopePlanMagic || plan->n_pairs < 1 || plan->n_pairs > H3B_ROPE_MAX_PAIRS ||
-      plan->n_axes < 1 || plan->n_axes > H3B_ROPE_MAX_AXES)
+      plan->n_axes < 1 || plan->n_axes > H3B_ROPE_MAX_AXES ||
+      (plan->pairing == H3B_ROPE_HALVES && plan->n_pairs % 4))
     return set_error(H3B_EINVAL, "%s: the plan was not made by h3b_rope_plan_make", who);
   if (2 * plan->n_pairs > head_dim)
     return set_error(H3B_EINVAL, "%s: the plan rotates %d channels of a head of %d", who,
@@ -1705,7 +1706,9 @@ size_t h3b_attention_prefix_workspace_size(int batch, int n_q, int n_heads, int 
   a.kv_heads = n_kv_heads;
   a.n_prefix = n_prefix;
   a.n_kv = n_kv;
-  return prefix_workspace_bytes(a, head_dim);
+  const size_t need = prefix_workspace_bytes(a, head_dim);
+  if (need == 0) set_error(H3B_EINVAL, "attention_prefix: too much work for one call");
+  return need;
 }
 
 int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view* k_prefix,
@@ -1732,6 +1735,7 @@ int h3b_attention_prefix(int dtype, const h3b_head_view* q, const h3b_head_view*
   if (!al4(kv_len) || !al4(q_len)) return set_error(H3B_EINVAL, "%s: misaligned lengths", me);
   const size_t need = h3b_attention_prefix_workspace_size(batch, n_q, n_heads, n_kv_heads, head_dim,
                                                           n_prefix, n_kv);
+  if (need == 0) return H3B_EINVAL;
   if (!ws || !al16(ws) || ws_bytes < need)
     return set_error(H3B_EWORKSPACE, "%s: workspace of %zu bytes needed, %zu given (16-byte aligned)",
                      me, need, ws ? ws_bytes : size_t(0));

@@ -168,7 +168,7 @@ struct HeadRows {
   int n_axes = 0;
   int n_pairs = 0;             // 0: no rotation
   int inverse = 0;
-  int parts[2] = {1, 1};       // set by the launcher: warps that share a token's heads,
+  int parts[2] = {1, 1};       // set by the launcher: items that a token's heads make,
   int q_blocks = 0;            // and the blocks that work on q
   const float* pos = nullptr;  // [(batch,) tokens, n_axes]
   long long pos_batch = 0;
@@ -218,7 +218,8 @@ struct PrefixArgs {
   uint32_t* err = nullptr;
 };
 
-// Sizes of a (batch, n_q, heads, kv_heads, n_prefix, n_kv) are all it reads.
+// Sizes of a (batch, n_q, heads, kv_heads, n_prefix, n_kv) are all it reads.  0: more work than a
+// schedule counts.
 size_t prefix_workspace_bytes(PrefixArgs a, int head_dim);
 int launch_attention_prefix(const DevCtx& ctx, bool fp16, int head_dim, PrefixArgs a, void* ws,
                             cudaStream_t stream);

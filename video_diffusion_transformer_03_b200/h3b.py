@@ -664,6 +664,8 @@ def _lead(t, name: str):
 
 
 def _heads(t, name: str, shape, dtype, dev: int) -> HeadView:
+    if t is None:
+        raise TypeError(f"{name}: a tensor is needed")
     s = t.stride()
     if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype} on cuda:{dev}, got "
