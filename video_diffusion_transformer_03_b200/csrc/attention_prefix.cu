@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(384, 1)
 // with 2,048 own keys each and next to no prefix 0.93 to 0.95.  Two sequences of 4 heads of 64 over
 // 257 keys take 11 us: launch, schedule, cold instructions and the join.  A unit of a single step
 // costs its CTA some 2.6 us, which bounds many short own caches (2,048 sequences of about 115 own
-// keys over 4,096 shared ones: 600 us, 0.26).
+// keys over 4,096 shared ones: 530 us, 0.29).
 
 template <int HD>
 struct NarrowCfg {
@@ -735,8 +735,8 @@ __device__ inline NarrowWalk narrow_first(const PrefixArgs& a, int lane, int cta
   w.end = all.begin(cta + 1);
   w.more = w.end > w.begin;
   if (w.begin < far) {
-    w.u.index = w.begin / narrow_work(a.prefix_tiles);
-    w.u.base = w.u.index * narrow_work(a.prefix_tiles);
+    w.u.index = w.begin / narrow_far_work(a);
+    w.u.base = w.u.index * narrow_far_work(a);
     w.u.b = -1;
     w.u.steps = a.prefix_tiles;
   } else {
@@ -1122,13 +1122,14 @@ __device__ __forceinline__ Side narrow_side(const PrefixArgs& a, const Cut& all,
                                             int base, int steps, int in_unit) {
   Side s;
   NarrowUnit u;
+  u.b = far ? -1 : 0;
   u.base = base;
   u.steps = steps;
   // a CTA at either end may hold some of the unit's range but no step of it
   s.c0 = all.cta_of(base);
-  int c1 = all.cta_of(base + narrow_work(steps) - 1);
-  if (narrow_step_at(u, all.begin(s.c0 + 1)) == 0) ++s.c0;
-  if (narrow_step_at(u, all.begin(c1)) == steps) --c1;
+  int c1 = all.cta_of(base + narrow_work(a, u) - 1);
+  if (narrow_step_at(a, u, all.begin(s.c0 + 1)) == 0) ++s.c0;
+  if (narrow_step_at(a, u, all.begin(c1)) == steps) --c1;
   s.n = 2 * (c1 - s.c0 + 1);
   s.row = narrow_row(a, far, index, s.c0, 0) + in_unit;
   s.chain = size_t(a.gt) * a.n_q * (far ? a.bt : 1);
@@ -1192,7 +1193,7 @@ __global__ void __launch_bounds__(128) k_prefix_join(const __grid_constant__ Pre
       const int g = h - kvh * a.group - hg * a.gt, hh = kvh * a.head_groups + hg;
       if (a.prefix_units > 0) {
         const int chunk = b / a.bt, index = hh * a.chunks + chunk;
-        side[0] = narrow_side(a, all, true, index, index * narrow_work(a.prefix_tiles), a.prefix_tiles,
+        side[0] = narrow_side(a, all, true, index, index * narrow_far_work(a), a.prefix_tiles,
                               ((b - chunk * a.bt) * a.gt + g) * a.n_q + tok);
       }
       const int steps = narrow_steps(len);
@@ -1315,7 +1316,7 @@ int launch_wide(const DevCtx& ctx, PrefixArgs a, cudaStream_t stream) {
 }
 
 // Blocks of the join an SM gets at most; a block sums the batch's lengths once, for all its rows.
-// 2,048 sequences of 24 heads: 600 us, with a block for every four rows 819.
+// 2,048 sequences of 24 heads: 600 us when it came, with a block for every four rows 819.
 constexpr long long kJoinBlocks = 16;
 
 template <typename T, int HD>
@@ -1367,6 +1368,7 @@ void narrow_units(PrefixArgs& a) {
   a.chunks = (a.batch + a.bt - 1) / a.bt;
   a.bt = (a.batch + a.chunks - 1) / a.chunks;
   a.own_units = a.kv_heads * a.head_groups;
+  a.far_step = narrow_far_step(a.bt * a.gt * a.n_q);
   a.prefix_units = a.n_prefix > 0 ? a.own_units * a.chunks : 0;
 }
 

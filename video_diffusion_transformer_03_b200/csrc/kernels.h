@@ -208,6 +208,7 @@ struct PrefixArgs {
   // narrow form: query heads and sequences of a unit, and the units' counts
   int gt = 1, head_groups = 1, bt = 1, chunks = 1;
   int prefix_units = 0, own_units = 0;
+  int far_step = 0;             // cost of a step of the prefix
   int ctas = 0;
   float* part_rows = nullptr;   // [slot][rows][head_dim] O, prefix slots then own ones
   float2* part_sums = nullptr;  // [slot][rows] (running max, row sum)

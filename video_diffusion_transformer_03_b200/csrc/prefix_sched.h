@@ -160,9 +160,13 @@ inline double wide_work_cap(const PrefixArgs& a) {
 // every sequence's own, (sequence, key head, group of query heads).  A unit's rows are its
 // sequences' queries of those heads; its steps the 128-key tiles of the prefix or of the
 // sequence.  Units without keys or queries have no work.
-// Cost of a step, and of a unit's start and end.  A unit at 8, 6 and 3: 512 sequences of one step
-// each over 4,096 shared keys 178, 161 and 136 us, 48 of 1 to 16 steps over 16,133 69, 69 and 76.
-constexpr int kNarrowStep = 4, kNarrowUnit = 6;
+// Cost of a step and of a unit's start and end, and of a step of the prefix where its rows take
+// all four quarters of tensor memory.  Measured, us (unit, full step): 512 sequences of 24 / 8
+// heads with one step each over 4,096 shared keys (126 rows) 180 (16, 8), 163 (12, 8), 146 (12, 10),
+// 150 (12, 13); 48 with 1 to 16 steps over 16,133 (72 rows) 69 with a unit of 12 or 16, 76 with 6.
+constexpr int kOwnStep = 8, kNarrowUnit = 12;
+constexpr int kFarFull = 10;
+inline int narrow_far_step(int rows) { return rows > 96 ? kFarFull : kOwnStep; }
 
 struct NarrowUnit {
   int index;        // prefix units, then batch x own units
@@ -174,19 +178,27 @@ struct NarrowUnit {
 };
 
 __host__ __device__ inline int narrow_work(int steps) {
-  return steps > 0 ? kNarrowUnit + steps * kNarrowStep : 0;
+  return steps > 0 ? kNarrowUnit + steps * kOwnStep : 0;
+}
+__host__ __device__ inline int narrow_far_work(const PrefixArgs& a) {
+  return kNarrowUnit + a.prefix_tiles * a.far_step;
+}
+__host__ __device__ inline int narrow_work(const PrefixArgs& a, const NarrowUnit& u) {
+  return u.b < 0 ? narrow_far_work(a) : narrow_work(u.steps);
 }
 __host__ __device__ inline int narrow_steps(const Lens& l) {
   return l.q > 0 ? (l.kv + 127) / 128 : 0;
 }
 __host__ __device__ inline int narrow_prefix_work(const PrefixArgs& a) {
-  return a.prefix_units * narrow_work(a.prefix_tiles);
+  return a.prefix_units * narrow_far_work(a);
 }
 
-__host__ __device__ inline int narrow_step_at(const NarrowUnit& u, int pos) {
+__host__ __device__ inline int narrow_step_at(const PrefixArgs& a, const NarrowUnit& u, int pos) {
   const int r = pos - u.base - kNarrowUnit;
   if (r <= 0) return 0;
-  const int j = (r + kNarrowStep - 1) / kNarrowStep;
+  // (either divisor a constant: a shift or a multiplication)
+  const bool full = u.b < 0 && a.far_step == kFarFull;
+  const int j = full ? (r + kFarFull - 1) / kFarFull : (r + kOwnStep - 1) / kOwnStep;
   return j < u.steps ? j : u.steps;
 }
 
@@ -205,7 +217,7 @@ __host__ __device__ inline bool narrow_own(const PrefixArgs& a, NarrowUnit& u, i
 }
 
 __host__ __device__ inline bool narrow_next(const PrefixArgs& a, NarrowUnit& u) {
-  u.base += narrow_work(u.steps);
+  u.base += narrow_work(a, u);
   if (u.b < 0) {
     if (++u.index < a.prefix_units) return true;
     return narrow_own(a, u, 0);
@@ -219,7 +231,7 @@ __host__ __device__ inline bool narrow_next(const PrefixArgs& a, NarrowUnit& u) 
 
 // CTAs that get a range: as many as there are, but at least min_work for each.
 __host__ __device__ inline int narrow_ctas(int total, int most) {
-  const int n = total / (2 * kNarrowStep + kNarrowUnit);
+  const int n = total / (2 * kOwnStep + kNarrowUnit);
   return n < 1 ? 1 : n < most ? n : most;
 }
 
@@ -231,22 +243,22 @@ struct NarrowWalk {
 
   __host__ __device__ inline void settle(const PrefixArgs& a) {
     while (more) {
-      j0 = narrow_step_at(u, begin);
-      j1 = narrow_step_at(u, end);
+      j0 = narrow_step_at(a, u, begin);
+      j1 = narrow_step_at(a, u, end);
       if (j0 < j1) return;
-      more = u.base + narrow_work(u.steps) < end && narrow_next(a, u);
+      more = u.base + narrow_work(a, u) < end && narrow_next(a, u);
     }
   }
   __host__ __device__ inline void next(const PrefixArgs& a) {
-    more = u.base + narrow_work(u.steps) < end && narrow_next(a, u);
+    more = u.base + narrow_work(a, u) < end && narrow_next(a, u);
     settle(a);
   }
 };
 
 inline long long narrow_work_cap(const PrefixArgs& a) {
   const long long far = (a.n_prefix + 127) / 128, own = (a.n_kv + 127) / 128;
-  return a.prefix_units * (kNarrowUnit + far * kNarrowStep) +
-         1ll * a.batch * a.own_units * (kNarrowUnit + own * kNarrowStep);
+  return a.prefix_units * (kNarrowUnit + far * a.far_step) +
+         1ll * a.batch * a.own_units * (kNarrowUnit + own * kOwnStep);
 }
 
 }  // namespace h3b
