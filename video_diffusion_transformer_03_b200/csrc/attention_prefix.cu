@@ -42,7 +42,10 @@ namespace {
 
 constexpr uint32_t kBox = 128 * 128;  // 128 rows of 128 bytes, swizzled
 constexpr int kRing = 3;
-constexpr int kMaxPieces = 8;  // CTAs that share a unit, on average, at most
+// CTAs that share a unit, on average, at most: the one that joins the states reads them one after
+// the other.  With 8, 4 and 3, us: one sequence of 12 heads and 127 queries over 2,712 keys 34, 27
+// and 27; 512 queries of 6 heads over 4,096 45, 41 and 44; two of 100 over 8,000 45, 41 and 47.
+constexpr int kMaxPieces = 4;
 
 template <int HD>
 struct WideCfg {
