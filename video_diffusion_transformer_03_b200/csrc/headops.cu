@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_ro
   const HeadView in = a.in[w], out = a.out[w];
   const int heads = a.heads[w], parts = a.parts[w];
   const int groups = (heads + kGroup - 1) / kGroup;
-  const int each = (groups + parts - 1) / parts;  // of an item (the last may have fewer)
   const unsigned n_items = static_cast<unsigned>(a.rows) * parts;
 
   // this lane computes kOwn of its slot's angles; lanes of the other heads the others
@@ -334,6 +333,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_ro
     if (parts > 1) {
       row = item / parts;
       const int part = static_cast<int>(item - row * parts);
+      const int each = (groups + parts - 1) / parts;  // (the last item may have fewer)
       g0 = part * each;
       g1 = min(groups, g0 + each);
     }
