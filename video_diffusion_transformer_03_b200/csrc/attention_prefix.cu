@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t s_addr = tmem + lane_addr + w * 128;
     const uint32_t o_addr = tmem + lane_addr + kOCol + w * 128;
     const float sl2 = a.scale_log2;
-    uint8_t* pbuf = sP + w * Cfg::kPBytes + row * 128;
+    uint4* pbuf = reinterpret_cast<uint4*>(sP + w * Cfg::kPBytes);
     bool ok = true;
     int c = 0;  // steps of this tile so far
     int t = 0;  // steps of this CTA so far (ring position)
@@ -504,11 +504,9 @@ __global__ void __launch_bounds__(384, 1)
           if (!ok) break;
         }
 #pragma unroll
-        for (int c16 = 0; c16 < 16; ++c16) {
-          const int chunk = (c16 & 7) ^ (row & 7);
-          *reinterpret_cast<uint4*>(pbuf + (c16 >> 3) * kBox + chunk * 16) =
+        for (int c16 = 0; c16 < 16; ++c16)
+          pbuf[tile_piece(row, c16)] =
               make_uint4(pk[c16 * 4], pk[c16 * 4 + 1], pk[c16 * 4 + 2], pk[c16 * 4 + 3]);
-        }
         if (j > wk.j0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
           tc_fence_after();
 #pragma unroll 1
@@ -595,7 +593,6 @@ __global__ void __launch_bounds__(384, 1)
         }
         const float inv_l = m == -INFINITY ? 0.0f : 1.0f / l;  // 0: the row sees no key
         constexpr int kVecs = HD / 8;  // 16-byte pieces of a row
-        uint4* stage = reinterpret_cast<uint4*>(sP + w * Cfg::kPBytes);
 #pragma unroll 1
         for (int cc = 0; cc < HD / 32; ++cc) {
           float o[32];
@@ -620,7 +617,8 @@ __global__ void __launch_bounds__(384, 1)
               o[4 * i + 3] = fmaf(v.w, wa, o[4 * i + 3]);
             }
           }
-          // to this row of the P tile, which is free: 16 bytes at a time, rotated by the row
+          // to where this row's P was, 16 bytes at a time.  A warp writes and reads back its own
+          // 32 rows of P only: one that is ahead may be storing the next segment's
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint4 u;
@@ -628,7 +626,7 @@ __global__ void __launch_bounds__(384, 1)
             u.y = pack2<T>(o[8 * i + 2] * inv_l, o[8 * i + 3] * inv_l);
             u.z = pack2<T>(o[8 * i + 4] * inv_l, o[8 * i + 5] * inv_l);
             u.w = pack2<T>(o[8 * i + 6] * inv_l, o[8 * i + 7] * inv_l);
-            stage[row * kVecs + ((cc * 4 + i + row) & (kVecs - 1))] = u;
+            pbuf[tile_piece(row, cc * 4 + i)] = u;
           }
         }
         // and from there whole rows at a time: the warp's own 32, those past q_len left out
@@ -637,7 +635,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 4
         for (int i = 0; i < kVecs; ++i) {
           const int r = quarter * 32 + (i * 32 + lane) / kVecs, v = lane & (kVecs - 1);
-          const uint4 u = stage[r * kVecs + ((v + r) & (kVecs - 1))];
+          const uint4 u = pbuf[tile_piece(r, v)];
           if (q0 + r < wk.u.len.q)
             *reinterpret_cast<uint4*>(dst + static_cast<long long>(q0 + r) * a.out.token + v * 8) = u;
         }

@@ -1,6 +1,6 @@
 // The schedules of the shared-prefix attention: how the work of a batch is cut into one range
-// per CTA, and the walk over a range, of its wide and of its narrow form.  Host and device, so
-// that they can be enumerated without a GPU.
+// per CTA, and the walk over a range, of its wide and of its narrow form; and where the rows of a
+// swizzled tile lie.  Host and device, so that they can be enumerated without a GPU.
 #pragma once
 
 #include "kernels.h"
@@ -12,6 +12,12 @@ constexpr int kBlockQ = 256;
 constexpr long long kMaxWork = (1ll << 31) - 1;
 
 __host__ __device__ inline int clamp_len(int v, int top) { return v < 0 ? 0 : v > top ? top : v; }
+
+// Where the 16-byte piece `piece` of row `row` lies in a tile of 128 rows in boxes of 128 bytes a
+// row, swizzled as the tensor core reads them; in pieces.
+__host__ __device__ inline int tile_piece(int row, int piece) {
+  return (piece >> 3) * (128 * 8) + row * 8 + ((piece & 7) ^ (row & 7));
+}
 
 struct Lens {
   int q, kv;
