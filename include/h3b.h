@@ -635,10 +635,10 @@ size_t h3b_qk_norm_rope_backward_workspace_size(int head_dim);
 
 /* The backward pass of h3b_qk_norm_rope: from its inputs q, k and the gradients g_q, g_k of
  * its outputs, the gradients dq, dk (overwritten) and those of the gains dq_gain, dk_gain
- * [head_dim] fp32 (overwritten; NULL = not wanted).  dq may be q or g_q itself (the same
- * view), dk likewise; otherwise outputs must not overlap inputs.  The gains' gradients are
- * summed in fp32 in a fixed order: equal calls give equal bits.  ws: device, 16-byte aligned,
- * h3b_qk_norm_rope_backward_workspace_size bytes, used by one call at a time. */
+ * [head_dim] fp32 (overwritten; NULL = not wanted; without k dk_gain becomes zero).  dq may be
+ * q or g_q itself (the same view), dk likewise; otherwise outputs must not overlap inputs.  The
+ * gains' gradients are summed in fp32 in a fixed order: equal calls give equal bits.  ws: device,
+ * 16-byte aligned, h3b_qk_norm_rope_backward_workspace_size bytes, used by one call at a time. */
 int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_head_view* q,
                               const h3b_head_view* k, int batch, int n_tokens, int n_q_heads,
                               int n_k_heads, int head_dim, const float* q_gain,

@@ -752,7 +752,10 @@ def _k_shape(shape, k):
 def qk_norm_rope(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos, q_out, k_out,
                  stream=None) -> None:
     """RMS norm of every head of q and k (gains [head_dim] fp32 or None), then the rotation
-    of rope_axes (plan None: none).  k may have fewer heads than q, or be None."""
+    of rope_axes (plan None: none, pos is ignored).  k may have fewer heads than q, or be None
+    (then k_out too)."""
+    if k is None and k_out is not None:
+        raise ValueError("k_out is given without k")
     shape, dtype, dev = _lead(q, "q")
     hd = shape[-1]
     pp, ps = _positions(plan, pos, shape, dev)
@@ -777,7 +780,10 @@ def qk_norm_rope_backward_workspace_size(head_dim: int) -> int:
 def qk_norm_rope_backward(plan: Optional[RopePlan], q, k, q_gain, k_gain, eps: float, pos, g_q,
                           g_k, dq, dk, dq_gain, dk_gain, ws, stream=None) -> None:
     """Gradients of qk_norm_rope: from its inputs and the gradients g_q, g_k of its outputs to
-    dq, dk (may be g_q, g_k) and dq_gain, dk_gain [head_dim] fp32 (None: not wanted)."""
+    dq, dk (may be g_q, g_k) and dq_gain, dk_gain [head_dim] fp32 (None: not wanted).  Without
+    k, g_k and dk are None too, and dk_gain becomes zero."""
+    if k is None and (g_k is not None or dk is not None):
+        raise ValueError(f"{'dk' if g_k is None else 'g_k'} is given without k")
     shape, dtype, dev = _lead(q, "q")
     hd = shape[-1]
     pp, ps = _positions(plan, pos, shape, dev)
@@ -810,10 +816,14 @@ def attention_prefix(q, k_prefix, v_prefix, k, v, out, kv_len=None, q_len=None,
                      causal: bool = False, scale: float = 0.0, ws=None, stream=None) -> None:
     """out = attention of q [batch, n_q, heads, head_dim] over the shared k_prefix, v_prefix
     [n_prefix, kv_heads, head_dim] and the first kv_len[b] (int32 [batch], None: all) of each
-    sequence's own k, v [batch, n_kv, kv_heads, head_dim]; either pair may be None.  causal:
-    the queries are the last q_len[b] tokens of their sequence.  Rows from q_len[b] (None:
-    n_q) on are left as they were.  scale 0: 1 / sqrt(head_dim).  ws: a device buffer of
-    attention_prefix_workspace_size bytes."""
+    sequence's own k, v [batch, n_kv, kv_heads, head_dim]; either pair may be None (both of it;
+    kv_len goes with k).  causal: the queries are the last q_len[b] tokens of their sequence.
+    Rows from q_len[b] (None: n_q) on are left as they were.  scale 0: 1 / sqrt(head_dim).  ws:
+    a device buffer of attention_prefix_workspace_size bytes."""
+    if k_prefix is None and v_prefix is not None:
+        raise ValueError("v_prefix is given without k_prefix")
+    if k is None and (v is not None or kv_len is not None):
+        raise ValueError(f"{'kv_len' if v is None else 'v'} is given without k")
     shape, dtype, dev = _lead(q, "q")
     if len(shape) != 4:
         raise TypeError(f"q: expected [batch, n_q, heads, head_dim], got {tuple(shape)}")
