@@ -42,10 +42,6 @@ namespace {
 
 constexpr uint32_t kBox = 128 * 128;  // 128 rows of 128 bytes, swizzled
 constexpr int kRing = 3;
-// CTAs that share a unit, on average, at most: the one that joins the states reads them one after
-// the other.  With 8, 4 and 3, us: one sequence of 12 heads and 127 queries over 2,712 keys 34, 27
-// and 27; 512 queries of 6 heads over 4,096 45, 41 and 44; two of 100 over 8,000 45, 41 and 47.
-constexpr int kMaxPieces = 4;
 
 template <int HD>
 struct WideCfg {
@@ -573,7 +569,7 @@ __global__ void __launch_bounds__(384, 1)
         int lo = me;
         float wb = 1.0f;
         if (wk.j0 > 0) {
-          while (lo > 0 && all.begin(lo) > wk.u.base) --lo;
+          lo = first_cta(wk.u, all, me);
           float top = m;
           for (int from = lo; from < me && ok; ++from) {
             if (!has_piece(wk.u, all, from)) continue;
@@ -790,16 +786,6 @@ __device__ __forceinline__ NarrowHeads narrow_heads(const PrefixArgs& a, const N
   r.kvh = hh / a.head_groups;
   r.h0 = r.kvh * a.group + (hh - r.kvh * a.head_groups) * a.gt;
   return r;
-}
-
-// Where a segment's state goes: slots of the prefix hold bt * gt * n_q rows, own ones gt * n_q;
-// CTA + unit is different for every segment.
-__device__ __forceinline__ size_t narrow_row(const PrefixArgs& a, bool far, int index, int cta,
-                                             int chain) {
-  const size_t own_rows = size_t(a.gt) * a.n_q, far_rows = own_rows * a.bt;
-  const size_t far_slots = a.prefix_units > 0 ? size_t(a.prefix_units) + a.ctas : 0;
-  if (far) return (size_t(index + cta) * 2 + chain) * far_rows;
-  return far_slots * 2 * far_rows + (size_t(index - a.prefix_units + cta) * 2 + chain) * own_rows;
 }
 
 template <typename T, int HD>
@@ -1111,33 +1097,6 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-// The states of one side (the prefix, the own keys) of a row: CTAs c0 .. c1 hold the unit's
-// steps, two chains each; state i is chain i & 1 of CTA c0 + (i >> 1).
-struct Side {
-  int c0, n;         // n states
-  size_t row, step;  // row of state 0 in the workspace, and from one CTA's to the next
-  size_t chain;      // from chain 0's to chain 1's
-};
-
-__device__ __forceinline__ Side narrow_side(const PrefixArgs& a, const Cut& all, bool far, int index,
-                                            int base, int steps, int in_unit) {
-  Side s;
-  NarrowUnit u;
-  u.b = far ? -1 : 0;
-  u.base = base;
-  u.steps = steps;
-  // a CTA at either end may hold some of the unit's range but no step of it
-  s.c0 = all.cta_of(base);
-  int c1 = all.cta_of(base + narrow_work(a, u) - 1);
-  if (narrow_step_at(a, u, all.begin(s.c0 + 1)) == 0) ++s.c0;
-  if (narrow_step_at(a, u, all.begin(c1)) == steps) --c1;
-  s.n = 2 * (c1 - s.c0 + 1);
-  s.row = narrow_row(a, far, index, s.c0, 0) + in_unit;
-  s.chain = size_t(a.gt) * a.n_q * (far ? a.bt : 1);
-  s.step = 2 * s.chain;
-  return s;
-}
-
 // Joins the states of a row of the output: WARPS warps per (sequence, query, head), each with
 // its share of the channels, lanes over those and over the states.  Launched while k_prefix_narrow runs: the
 // first rows' schedule is worked out before the wait for it, only the states' two loads come
@@ -1308,9 +1267,7 @@ int launch_wide(const DevCtx& ctx, PrefixArgs a, cudaStream_t stream) {
   auto kernel = k_prefix_wide<T, HD>;
   static std::atomic<uint64_t> done{0};
   if (int rc = allow_smem(ctx, kernel, Cfg::kSmem, done)) return rc;
-  const long long units = 1ll * a.batch * a.heads * ((a.n_q + kBlockQ - 1) / kBlockQ);
-  const int grid = static_cast<int>(
-      std::min<long long>(units * kMaxPieces, std::min(ctx.num_sms, kMaxSkCtas)));
+  const int grid = wide_ctas(a, std::min(ctx.num_sms, kMaxSkCtas));
   a.seq = next_scratch_seq();
   kernel<<<grid, 384, Cfg::kSmem, stream>>>(tm, a);
   return check_launch("attention_prefix");
@@ -1358,39 +1315,6 @@ int launch_narrow(const DevCtx& ctx, const PrefixArgs& a, cudaStream_t stream) {
 template <typename T, int HD>
 int launch_form(const DevCtx& ctx, const PrefixArgs& a, bool narrow, cudaStream_t stream) {
   return narrow ? launch_narrow<T, HD>(ctx, a, stream) : launch_wide<T, HD>(ctx, a, stream);
-}
-
-// The narrow form's units.
-void narrow_units(PrefixArgs& a) {
-  a.gt = std::min(a.group, 128 / a.n_q);
-  a.head_groups = (a.group + a.gt - 1) / a.gt;
-  a.gt = (a.group + a.head_groups - 1) / a.head_groups;
-  a.bt = a.n_prefix > 0 ? std::min(a.batch, 128 / (a.gt * a.n_q)) : 1;
-  a.chunks = (a.batch + a.bt - 1) / a.bt;
-  a.bt = (a.batch + a.chunks - 1) / a.chunks;
-  a.own_units = a.kv_heads * a.head_groups;
-  a.far_step = narrow_far_step(a.bt * a.gt * a.n_q);
-  a.prefix_units = a.n_prefix > 0 ? a.own_units * a.chunks : 0;
-}
-
-// Rows of the narrow form's workspace.
-size_t narrow_rows(const PrefixArgs& a) {
-  const size_t own = size_t(a.gt) * a.n_q;
-  size_t rows = 2 * (size_t(a.batch) * a.own_units + kMaxSkCtas) * own;
-  if (a.prefix_units > 0) rows += 2 * (size_t(a.prefix_units) + kMaxSkCtas) * own * a.bt;
-  return rows;
-}
-
-// The narrow form, for at most this many queries a sequence.  Narrow and wide, in us, 8 sequences
-// over 4,096 shared keys and 1,000 of their own: 24 / 8 heads 22 and 94 with one query, 50 and 94
-// with 32, 90 and 94 with 64, 115 and 95 with 96; 24 / 24 heads 77 and 97 with 64, 116 and 97 with
-// 96.  (The second limit below keeps its workspace and its schedule small.)
-constexpr int kNarrowQueries = 64;
-
-bool use_narrow(PrefixArgs a) {
-  if (a.n_q > kNarrowQueries || 1ll * a.batch * a.heads > (1 << 20)) return false;
-  narrow_units(a);
-  return narrow_work_cap(a) * 2 <= kMaxWork;
 }
 
 }  // namespace

@@ -5,6 +5,8 @@
 
 #include "kernels.h"
 
+#include <algorithm>
+
 namespace h3b {
 
 constexpr int kBlockQ = 256;
@@ -155,6 +157,21 @@ struct Walk {
   }
 };
 
+// The first CTA that may hold steps of the unit, whose last step is `me`'s.
+__host__ __device__ inline int first_cta(const Unit& u, const Cut& c, int me) {
+  while (me > 0 && c.begin(me) > u.base) --me;
+  return me;
+}
+
+// CTAs that share a unit, on average, at most: the one that joins the states reads them one after
+// the other.  With 8, 4 and 3, us: one sequence of 12 heads and 127 queries over 2,712 keys 34, 27
+// and 27; 512 queries of 6 heads over 4,096 45, 41 and 44; two of 100 over 8,000 45, 41 and 47.
+constexpr int kMaxPieces = 4;
+inline int wide_ctas(const PrefixArgs& a, int most) {
+  const long long units = 1ll * a.batch * a.heads * ((a.n_q + kBlockQ - 1) / kBlockQ);
+  return static_cast<int>(std::min<long long>(units * kMaxPieces, most));
+}
+
 // The most work a call of these sizes can have (in 64 bits the largest would not fit).
 inline double wide_work_cap(const PrefixArgs& a) {
   const double tiles = (a.n_prefix + 127) / 128 + (a.n_kv + 127) / 128;
@@ -235,9 +252,13 @@ __host__ __device__ inline bool narrow_next(const PrefixArgs& a, NarrowUnit& u) 
   return narrow_own(a, u, u.b + 1);
 }
 
-// CTAs that get a range: as many as there are, but at least min_work for each.
+// CTAs that get a range: as many as there are, but at least kMinRange for each.
+constexpr int kMinRange = 2 * kOwnStep + kNarrowUnit;
+// A range longer than a unit's start and a step: at each end of a unit at most one CTA has some of
+// the unit's range and none of its steps (narrow_side leaves it out).
+static_assert(kMinRange > kNarrowUnit + kOwnStep && kMinRange > kNarrowUnit + kFarFull, "range too short");
 __host__ __device__ inline int narrow_ctas(int total, int most) {
-  const int n = total / (2 * kOwnStep + kNarrowUnit);
+  const int n = total / kMinRange;
   return n < 1 ? 1 : n < most ? n : most;
 }
 
@@ -265,6 +286,76 @@ inline long long narrow_work_cap(const PrefixArgs& a) {
   const long long far = (a.n_prefix + 127) / 128, own = (a.n_kv + 127) / 128;
   return a.prefix_units * (kNarrowUnit + far * a.far_step) +
          1ll * a.batch * a.own_units * (kNarrowUnit + own * kOwnStep);
+}
+
+// Where a segment's state goes: slots of the prefix hold bt * gt * n_q rows, own ones gt * n_q;
+// CTA + unit is different for every segment.
+__host__ __device__ inline size_t narrow_row(const PrefixArgs& a, bool far, int index, int cta,
+                                             int chain) {
+  const size_t own_rows = size_t(a.gt) * a.n_q, far_rows = own_rows * a.bt;
+  const size_t far_slots = a.prefix_units > 0 ? size_t(a.prefix_units) + a.ctas : 0;
+  if (far) return (size_t(index + cta) * 2 + chain) * far_rows;
+  return far_slots * 2 * far_rows + (size_t(index - a.prefix_units + cta) * 2 + chain) * own_rows;
+}
+
+// The states of one side (the prefix, the own keys) of a row: CTAs c0 .. c1 hold the unit's
+// steps, two chains each; state i is chain i & 1 of CTA c0 + (i >> 1).
+struct Side {
+  int c0, n;         // n states
+  size_t row, step;  // row of state 0 in the workspace, and from one CTA's to the next
+  size_t chain;      // from chain 0's to chain 1's
+};
+
+__host__ __device__ inline Side narrow_side(const PrefixArgs& a, const Cut& all, bool far, int index,
+                                            int base, int steps, int in_unit) {
+  Side s;
+  NarrowUnit u;
+  u.b = far ? -1 : 0;
+  u.base = base;
+  u.steps = steps;
+  // a CTA at either end may hold some of the unit's range but no step of it
+  s.c0 = all.cta_of(base);
+  int c1 = all.cta_of(base + narrow_work(a, u) - 1);
+  if (narrow_step_at(a, u, all.begin(s.c0 + 1)) == 0) ++s.c0;
+  if (narrow_step_at(a, u, all.begin(c1)) == steps) --c1;
+  s.n = 2 * (c1 - s.c0 + 1);
+  s.row = narrow_row(a, far, index, s.c0, 0) + in_unit;
+  s.chain = size_t(a.gt) * a.n_q * (far ? a.bt : 1);
+  s.step = 2 * s.chain;
+  return s;
+}
+
+// The narrow form's units.
+inline void narrow_units(PrefixArgs& a) {
+  a.gt = std::min(a.group, 128 / a.n_q);
+  a.head_groups = (a.group + a.gt - 1) / a.gt;
+  a.gt = (a.group + a.head_groups - 1) / a.head_groups;
+  a.bt = a.n_prefix > 0 ? std::min(a.batch, 128 / (a.gt * a.n_q)) : 1;
+  a.chunks = (a.batch + a.bt - 1) / a.bt;
+  a.bt = (a.batch + a.chunks - 1) / a.chunks;
+  a.own_units = a.kv_heads * a.head_groups;
+  a.far_step = narrow_far_step(a.bt * a.gt * a.n_q);
+  a.prefix_units = a.n_prefix > 0 ? a.own_units * a.chunks : 0;
+}
+
+// Rows of the narrow form's workspace.
+inline size_t narrow_rows(const PrefixArgs& a) {
+  const size_t own = size_t(a.gt) * a.n_q;
+  size_t rows = 2 * (size_t(a.batch) * a.own_units + kMaxSkCtas) * own;
+  if (a.prefix_units > 0) rows += 2 * (size_t(a.prefix_units) + kMaxSkCtas) * own * a.bt;
+  return rows;
+}
+
+// The narrow form, for at most this many queries a sequence.  Narrow and wide, in us, 8 sequences
+// over 4,096 shared keys and 1,000 of their own: 24 / 8 heads 22 and 94 with one query, 50 and 94
+// with 32, 90 and 94 with 64, 115 and 95 with 96; 24 / 24 heads 77 and 97 with 64, 116 and 97 with
+// 96.  (The second limit below keeps its workspace and its schedule small.)
+constexpr int kNarrowQueries = 64;
+
+inline bool use_narrow(PrefixArgs a) {
+  if (a.n_q > kNarrowQueries || 1ll * a.batch * a.heads > (1 << 20)) return false;
+  narrow_units(a);
+  return narrow_work_cap(a) * 2 <= kMaxWork;
 }
 
 }  // namespace h3b
