@@ -277,6 +277,9 @@ constexpr int blocks_per_sm(int mode, int C) {
   if (mode == kModeNorm) return C == 16 ? 5 : 6;
   return C == 16 ? 4 : 5;
 }
+// (the caller's workspace has a row for each of the backward pass's blocks)
+static_assert(blocks_per_sm(kModeNormBwd, 8) <= kHeadRowsBwdPerSm && blocks_per_sm(kModeNormBwd, 16) <= kHeadRowsBwdPerSm,
+              "backward workspace");
 
 template <typename T, int C, bool HALVES, int LPH, int MODE, bool WHOLE>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(MODE, C)) k_head_rows(const __grid_constant__ HeadRows a) {
