@@ -663,7 +663,9 @@ int h3b_qk_norm_rope_backward(const h3b_rope_plan* plan, int dtype, const h3b_he
  * No stride of q, k, v or the prefix may be 0 (dimensions of size 1 apart).
  * kv_len, q_len: device int32 [batch], read by the kernels (a captured graph follows their
  * values), clamped to [0, n_kv] and [0, n_q]; NULL: n_kv, n_q.  What lies in k, v behind
- * kv_len[b] is never used, whatever it holds.  scale > 0, or 0 for 1 / sqrt(head_dim).
+ * kv_len[b] is never used, whatever it holds.  In front of it, what a causal query does not see
+ * has weight 0: such keys may be anything, their values have to be finite (0 times an infinity is
+ * NaN).  scale > 0, or 0 for 1 / sqrt(head_dim); scores up to 10^7 in magnitude.
  * Scores, softmax and sums are fp32; the weights are rounded to the type for the product with
  * the values.  Equal calls give equal bits.
  * ws: device scratch, 16-byte aligned, of h3b_attention_prefix_workspace_size bytes; one call

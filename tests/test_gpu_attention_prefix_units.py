@@ -63,3 +63,38 @@ def test_many_short_units_repeat_their_bits():
     check(call(*host, q_len=rows), *host, q_len=rows)
     again = call(*host, q_len=rows, fill=0.0)
     assert torch.equal(again, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("nq", [1, 200])
+def test_large_scores_pick_their_key(nq, dtype):
+    """Scores up to 8e6, 2^10 apart and exact: the weight of the highest key is all there is.  It is
+    rounded to the type once and the output once, its sum is not: 2 u |v| + u |v|."""
+    heads, hd, prefix, nkv = 2, 64, 300, 200
+    rng = np.random.default_rng(5)
+    q = torch.zeros(1, nq, heads, hd)
+    q[..., 0] = 2.0 ** 15
+    # 500 different scores, an eighth of 2^13 .. 2^13 a key in steps that both types hold
+    steps = torch.tensor(rng.permutation(500).astype(np.float32)) / 2
+    k = torch.zeros(500, heads, hd)
+    k[..., 0] = steps[:, None]
+    v = torch.tensor(rng.standard_normal((500, heads, hd)).astype(np.float32)).to(dtype)
+    q, k = q.to(dtype), k.to(dtype)
+    # (types of 8 bits of mantissa merge some neighbours: keep the keys that stay alone on top)
+    top = int(k[:, 0, 0].float().argmax())
+    k[:, :, 0] = torch.where(torch.arange(500)[:, None] == top, k[:, :, 0],
+                             torch.clamp(k[:, :, 0].float(), max=240.0).to(dtype))
+    out = call(q, k[:prefix], v[:prefix], k[None, prefix:], v[None, prefix:], scale=1.0)
+    want = v[top].float()
+    u = torch.finfo(dtype).eps / 2
+    assert k[:, 0, 0].float().max() * 2.0 ** 15 > 8e6
+    assert ((out.float().cpu() - want).abs() <= 3 * u * want.abs() + u * 2 ** -10).all()
+
+
+@pytest.mark.parametrize("nq", [5, 150])
+def test_keys_that_a_causal_query_does_not_see_may_be_anything(nq):
+    q, kp, vp, k, v = make(2, nq, 4, 2, 64, 70, nq + 3, BF, seed=31)
+    clean = call(q, kp, vp, k, v, causal=True)
+    k[:, -1] = float("nan")                        # the last query's own key
+    out = call(q, kp, vp, k, v, causal=True)
+    assert torch.equal(out[:, :-1], clean[:, :-1]) and out[:, -1].isnan().all()
