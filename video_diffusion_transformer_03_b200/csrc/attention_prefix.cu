@@ -23,9 +23,11 @@
 // TMEM: S0 [0, 128), S1 [128, 256), O0 [256, 384), O1 [384, 512).  Shared memory: Q0, Q1, P0,
 // P1 and a ring of three K / V tiles in the order of use (K of step t + 1 before V of step t).
 // Measured on B200, bf16, 24 heads of 128: six clips of 1,600 queries and 900 to 1,600 own keys
-// over 1,024 shared ones 245 us, 872 TFLOP/s, 0.52 of the cuBLAS rate of 1,663; 11,344 tokens
-// over 1,024 1,589 us, 1,085 TFLOP/s.  A tile's S, softmax and P V are a chain; two of them share
-// the tensor core and the exponentials, and the card then draws about 920 W of its 1,000.
+// over 1,024 shared ones 243 to 256 us in a burst of calls, 0.52 of the cuBLAS rate of 1,663 TFLOP/s,
+// and 287 to 296 once the calls go on and the power limit lowers the clocks (0.51 of 1,413, cuBLAS's
+// then); 11,344 tokens over 1,024 1,597 us, 1,080 TFLOP/s, where cuDNN's attention over joined keys
+// takes 1,175.  A tile's S, softmax and P V are a chain; two of them share the tensor core and the
+// exponentials, which are busy 45% and 43% of the time: in between both wait for the chains.
 #include "kernels.h"
 #include "prefix_sched.h"
 #include "ptx.cuh"
@@ -676,7 +678,8 @@ __global__ void __launch_bounds__(384, 1)
 // their softmax (warps without rows only keep the barriers' count).
 // TMEM: S0 / P0 [0, 128), S1 / P1 [128, 256), O0 [256, 384), O1 [384, 512).
 // Measured on B200, bf16, one query, 24 / 8 heads of 128: 48 sequences of 1 to 2,011 own keys over
-// 16,133 shared ones 70 us, 0.57 of the copy rate (a step of the prefix is bound by its softmax);
+// 16,133 shared ones 70 us in a graph, 0.57 of the copy rate (75 to 81 in repeated calls; a step of
+// the prefix is bound by its softmax);
 // with 2,048 own keys each and next to no prefix 0.93 to 0.95.  Two sequences of 4 heads of 64 over
 // 257 keys take 11 us: launch, schedule, cold instructions and the join.  A unit of a single step
 // costs its CTA some 2.6 us, which bounds many short own caches (2,048 sequences of about 115 own

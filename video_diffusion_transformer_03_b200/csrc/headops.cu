@@ -22,12 +22,15 @@
 // Measured on B200 (CUDA graphs, inputs past the L2 or rotated), heads of 128, against the copy
 // rate of 6,555 GB/s:
 //   rotation, fp16, 2 x 11,344 tokens of 24 heads               48 us  0.89
-//   norm + rotation, bf16, 3 x 11,341 tokens of 24 + 8 heads   106 us  0.80
-//   its backward, fp16, 2 x 11,343 tokens of 24 + 8 heads      105 us  0.81
-//   at 1,600 tokens, bf16: rotation of 24 heads 6.9 us, norm + rotation of 24 + 24 13.4, backward
-//   18.6 (0.43 to 0.48)
-// Large calls are bound by HBM and, next to it, by the instructions that a byte costs.  At 1,600
-// tokens a warp has three or so items, and launch, ladder and first loads are 4 us of the time.
+//   norm + rotation, bf16, 3 x 11,341 tokens of 24 + 8 heads   107 us  0.79
+//   its backward, fp16, 2 x 11,343 tokens of 24 + 8 heads      106 us  0.80
+//   in 32 bits, norm + rotation of 11,341 tokens of 24 + 8      67 us  0.85, its backward 95, 0.90
+//   at 1,600 tokens, bf16: rotation of 24 heads 7.0 us, norm + rotation of 24 + 24 13.5, backward
+//   18.7 (0.43 to 0.48)
+// (The first three in calls from Python: 50, 110 and 109 to 113 us.)  Large calls wait for HBM: the
+// largest stall is the loads' (0.55 to 0.63 instructions issued a cycle), and registers limit how
+// many are in flight.  At 1,600 tokens a warp has three or so items, and launch, ladder and first
+// loads are 4 us of the time.
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -583,9 +586,9 @@ int launch(const DevCtx& ctx, HeadRows& a, cudaStream_t stream) {
   const int sms = std::min(ctx.num_sms, kMaxSkCtas);
   const long long most = 1ll * blocks_per_sm(MODE, C) * sms;
   // An item is a token's heads (of q, or of k).  Where tokens are too few to keep the SMs busy
-  // that way, it is `per` groups of them: the number for which the warps that fit would be done
-  // first, each going through its share of the items one after the other, every item computing
-  // its token's angles again.  At 300 tokens of 24 + 24 heads norm + rotation takes 4.8 us instead
+  // that way, it is `per` groups of them: of 1 to 8, 16, 32, ... the number for which the warps that
+  // fit would be done first, each going through its share of the items one after the other, every
+  // item computing its token's angles again.  At 300 tokens of 24 + 24 heads norm + rotation takes 4.8 us instead
   // of 6.0; at 3 x 11,341 tokens, where whole tokens are kept, the same choice costs 126 instead
   // of 106.
   int groups[2];

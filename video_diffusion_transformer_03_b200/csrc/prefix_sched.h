@@ -349,7 +349,14 @@ inline size_t narrow_rows(const PrefixArgs& a) {
 // The narrow form, for at most this many queries a sequence.  Narrow and wide, in us, 8 sequences
 // over 4,096 shared keys and 1,000 of their own: 24 / 8 heads 22 and 94 with one query, 50 and 94
 // with 32, 90 and 94 with 64, 115 and 95 with 96; 24 / 24 heads 77 and 97 with 64, 116 and 97 with
-// 96.  (The second limit below keeps its workspace and its schedule small.)
+// 96.  The narrow form's states, 8 * (HD / 2 + 1) bytes a row, side and chain, are written and read
+// back, so its cost and its workspace grow with the batch; over 4,096 shared and 256 own keys, heads
+// of 128, 16, 32 and 64 queries, narrow, and wide (which they hardly change):
+//   24 / 8 heads, 64 sequences 152, 362, 956 and 573; 256: 584, 1,392, 3,775 and 2,247
+//   24 / 24 heads, 64 sequences 152, 281, 590 and 579; 256: 560, 1,052, 2,312 and 2,260
+// With 33 to 64 queries of shared key heads the wide form would be the faster one; the rule has no
+// part for that yet.  The workspace there is 1.1 GB for 256 sequences of 64 queries.  The second
+// limit bounds the schedule's integers, not the workspace.
 constexpr int kNarrowQueries = 64;
 
 inline bool use_narrow(PrefixArgs a) {
