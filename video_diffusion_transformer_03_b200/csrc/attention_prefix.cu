@@ -25,8 +25,8 @@
 // Measured on B200, bf16, 24 heads of 128: six clips of 1,600 queries and 900 to 1,600 own keys
 // over 1,024 shared ones 243 to 256 us in a burst of calls, 0.52 of the cuBLAS rate of 1,663 TFLOP/s,
 // and 287 to 296 once the calls go on and the power limit lowers the clocks (0.51 of 1,413, cuBLAS's
-// then); 11,344 tokens over 1,024 1,597 us, 1,080 TFLOP/s, where cuDNN's attention over joined keys
-// takes 1,175.  A tile's S, softmax and P V are a chain; two of them share the tensor core and the
+// then); 11,344 tokens over 1,024 1,597 us, 1,080 TFLOP/s, where the vendor library's attention over
+// joined keys takes 1,175.  A tile's S, softmax and P V are a chain; two of them share the tensor core and the
 // exponentials, which are busy 45% and 43% of the time: in between both wait for the chains.
 #include "kernels.h"
 #include "prefix_sched.h"

@@ -281,7 +281,8 @@ constexpr int blocks_per_sm(int mode, int C) {
   return C == 16 ? 4 : 5;
 }
 // (the caller's workspace has a row for each of the backward pass's blocks)
-static_assert(blocks_per_sm(kModeNormBwd, 8) <= kHeadRowsBwdPerSm && blocks_per_sm(kModeNormBwd, 16) <= kHeadRowsBwdPerSm,
+static_assert(blocks_per_sm(kModeNormBwd, 8) <= kHeadRowsBwdPerSm &&
+                  blocks_per_sm(kModeNormBwd, 16) <= kHeadRowsBwdPerSm,
               "backward workspace");
 
 template <typename T, int C, bool HALVES, int LPH, int MODE, bool WHOLE>

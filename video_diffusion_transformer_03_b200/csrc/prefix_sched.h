@@ -256,7 +256,8 @@ __host__ __device__ inline bool narrow_next(const PrefixArgs& a, NarrowUnit& u) 
 constexpr int kMinRange = 2 * kOwnStep + kNarrowUnit;
 // A range longer than a unit's start and a step: at each end of a unit at most one CTA has some of
 // the unit's range and none of its steps (narrow_side leaves it out).
-static_assert(kMinRange > kNarrowUnit + kOwnStep && kMinRange > kNarrowUnit + kFarFull, "range too short");
+static_assert(kMinRange > kNarrowUnit + kOwnStep && kMinRange > kNarrowUnit + kFarFull,
+              "range too short");
 __host__ __device__ inline int narrow_ctas(int total, int most) {
   const int n = total / kMinRange;
   return n < 1 ? 1 : n < most ? n : most;
